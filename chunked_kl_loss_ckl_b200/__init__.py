@@ -10,6 +10,9 @@ is present.
     loss, lse = ckl.forward(H, W, idx, logp, mask, chunk=1024)
     dH, dW = ckl.backward(H, W, idx, logp, mask, lse, chunk=1024)
     loss = ckl.chunked_kl_loss(H, W, idx, logp, mask, chunk=1024)  # autograd
+
+The operators around the loss (the norm that makes H, 8-bit activations,
+sampling from logits; ``include/ckl_ops.h``) are in ``_ops``.
 """
 
 from __future__ import annotations
@@ -541,3 +544,9 @@ class _ChunkedKL(torch.autograd.Function):
 def chunked_kl_loss(H, W, idx, logp, mask=None, chunk: int = 1024):
     """Differentiable loss (gradients w.r.t. H and W; dW cast to W's dtype)."""
     return _ChunkedKL.apply(H, W, idx, logp, mask, chunk)
+
+
+from . import _ops  # noqa: E402  (needs the names above)
+from ._ops import *  # noqa: E402,F401,F403
+
+__all__ += _ops.__all__

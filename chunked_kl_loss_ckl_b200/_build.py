@@ -15,9 +15,9 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 LIB_PATH = os.path.join(PKG_DIR, "libckl.so")
-SOURCES = [os.path.join(CSRC, "ckl_api.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("ckl_api.cu", "ckl_ops.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh")] + [
-    os.path.join(ROOT, "include", "ckl.h")
+    os.path.join(ROOT, "include", f) for f in ("ckl.h", "ckl_ops.h")
 ]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]

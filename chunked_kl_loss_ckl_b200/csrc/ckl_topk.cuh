@@ -30,6 +30,7 @@
 
 #include <cstdint>
 
+#include "ckl_bf16.cuh"
 #include "ckl_ptx.cuh"
 
 #define CKL_DEV_TOPK_TIES 8  // more elements tie at the K-th logit than the sort holds
@@ -40,15 +41,6 @@ constexpr int TK_THREADS = 512;
 constexpr int TK_WIN = 4096;  // keys per histogram window
 constexpr int TK_WIN0 = 128;  // keys in the first window (one binade of bf16)
 constexpr int TK_CAP = 2048;  // elements the final sort holds (K plus the ties at the K-th)
-
-__device__ __forceinline__ uint32_t bf16_key(uint32_t b) {
-  if (b == 0x8000u) b = 0u;  // -0 == +0
-  return (b & 0x8000u) ? (~b & 0xFFFFu) : (b | 0x8000u);
-}
-__device__ __forceinline__ float key_value(uint32_t k) {
-  const uint32_t b = (k & 0x8000u) ? (k & 0x7FFFu) : (~k & 0xFFFFu);
-  return __uint_as_float(b << 16);
-}
 
 // Order-preserving keys of two packed bf16 values (each half as bf16_key).
 __device__ __forceinline__ uint32_t bf16_key2(uint32_t w) {
@@ -62,14 +54,6 @@ constexpr int TK_UNROLL = 2;  // independent 16-byte loads in flight per thread
 #define CKL_TS_UNROLL 4
 #endif
 constexpr int TS_UNROLL = CKL_TS_UNROLL;  // the same, in the streaming form's pass
-
-__device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
 // Largest logit of the row (packed bf16 maxima, two per instruction).
 __device__ __forceinline__ float tk_row_max(const uint16_t* z, int V, bool vec8) {
