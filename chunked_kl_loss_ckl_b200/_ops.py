@@ -12,12 +12,11 @@ from torch.autograd.function import once_differentiable
 from . import CKL_OK, LIB_PATH, CklError, _ptr, backward, forward, lib
 
 __all__ = [
-    "ACT8_GROUP", "NORM_MAX_D", "SAMPLE_BAD_INPUT", "act8_pack", "act8_unpack", "norm_forward",
+    "ACT8_GROUP", "SAMPLE_BAD_INPUT", "act8_pack", "act8_unpack", "norm_forward",
     "norm_backward", "norm_workspace_bytes", "layer_norm", "rms_norm", "norm_kl_loss", "sample",
 ]
 
 ACT8_GROUP = 32
-NORM_MAX_D = 32768
 SAMPLE_BAD_INPUT = 16
 
 _DTYPES = {torch.bfloat16: 0, torch.float32: 1}

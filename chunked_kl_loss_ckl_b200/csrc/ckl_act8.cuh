@@ -20,6 +20,7 @@
 #include <cuda_bf16.h>
 
 #include <cstdint>
+#include <type_traits>
 
 namespace ckl {
 
@@ -59,23 +60,13 @@ __device__ __forceinline__ Act8Scale act8_scale(uint32_t b) {
 }
 
 // q in the low byte.  1.5 2^23 + v rounds v to the nearest integer, ties to
-// even, and leaves its two's complement in the low bits (one FADD in place of
-// a conversion, which the SM issues at an eighth of the rate).
+// even, and leaves its two's complement in the low bits (no conversion
+// instruction, which the SM issues at an eighth of the rate).
 __device__ __forceinline__ uint32_t act8_q(float x, Act8Scale s) {
   float v = x * s.f1 * s.f2;
   v = fminf(fmaxf(v, -127.f), 127.f);  // the largest floats only
   const uint32_t q = __float_as_uint(v + 12582912.f) & 0xFFu;
   return (__float_as_uint(x) & 0x7FFFFFFFu) < 0x7F800000u ? q : 0x80u;
-}
-
-// Byte j of the packed word as its value.  2^23 + (q + 128) is the float whose
-// low byte is q ^ 0x80.
-template <int J>
-__device__ __forceinline__ float act8_value(uint32_t word, Act8Scale s) {
-  const uint32_t w = word ^ 0x80808080u;
-  const float f = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440 | J)) - 8388736.f;
-  const float v = f * s.f1 * s.f2;
-  return f == -128.f ? __int_as_float(0x7FC00000) : v;
 }
 
 __device__ __forceinline__ float act8_value1(int8_t q, Act8Scale s) {
@@ -95,6 +86,14 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
   return __float2bfloat16_rn(x);
 }
 
+// Largest magnitude bits of eight elements, non-finite ones included.
+__device__ __forceinline__ uint32_t act8_top8(const float (&v)[8]) {
+  uint32_t a = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) a = max(a, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+  return a;
+}
+
 // Eight consecutive elements as loaded: one 16-byte vector of bf16 or two of
 // float.
 template <typename T>
@@ -105,7 +104,17 @@ struct Raw8<__nv_bfloat16> {
   __device__ __forceinline__ void load(const __nv_bfloat16* p) {
     a = *reinterpret_cast<const uint4*>(p);
   }
+  // its 16-byte pieces, `piece` bytes apart
+  __device__ __forceinline__ void load_pieces(const uint8_t* p, uint32_t) {
+    a = *reinterpret_cast<const uint4*>(p);
+  }
   __device__ __forceinline__ void clear() { a = make_uint4(0, 0, 0, 0); }
+  // largest magnitude bits (as a float's), non-finite ones included
+  __device__ __forceinline__ uint32_t top() const {
+    const uint32_t k = 0x7FFF7FFFu;
+    const uint32_t m = __vmaxu2(__vmaxu2(a.x & k, a.y & k), __vmaxu2(a.z & k, a.w & k));
+    return max(m & 0xFFFF0000u, m << 16);
+  }
   __device__ __forceinline__ void get(float (&v)[8]) const {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
@@ -134,7 +143,16 @@ struct Raw8<float> {
     a = reinterpret_cast<const float4*>(p)[0];
     b = reinterpret_cast<const float4*>(p)[1];
   }
+  __device__ __forceinline__ void load_pieces(const uint8_t* p, uint32_t piece) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(p + piece);
+  }
   __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ uint32_t top() const {
+    float v[8];
+    get(v);
+    return act8_top8(v);
+  }
   __device__ __forceinline__ void get(float (&v)[8]) const {
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
@@ -150,35 +168,63 @@ struct Raw8<float> {
 };
 
 // Eight elements of one lane to 8 bits; the four lanes of an aligned quad hold
-// one group of 32 (all lanes of the warp take part).  Returns the exponent
-// byte; q is the eight bytes.
-__device__ __forceinline__ uint32_t act8_pack8(const float (&v)[8], uint2& q) {
-  uint32_t a = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) a = max(a, act8_mag(v[j]));
-  a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
-  a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
-  const uint32_t b = act8_byte(a);
-  const Act8Scale s = act8_inv_scale(b);
+// one group of 32.  `top` is act8_top8(v).  Returns the exponent byte; q is the
+// eight bytes.  Where the group is finite and both 2^(133 - b) and the sums
+// below are normal floats, one FMA scales and rounds an element:
+// v 2^(133 - b) + 1.5 2^23 has the integer in its low byte.
+__device__ __forceinline__ uint32_t act8_pack8(const float (&v)[8], uint32_t top, uint2& q) {
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  uint32_t b = act8_byte(top);
   uint32_t w[2];
+  if (b >= 7u && b <= 253u && top < 0x7F800000u) {
+    const float f = pow2f(133 - static_cast<int>(b));
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-    w[h] = act8_q(v[4 * h], s) | (act8_q(v[4 * h + 1], s) << 8) | (act8_q(v[4 * h + 2], s) << 16) |
-           (act8_q(v[4 * h + 3], s) << 24);
+    for (int h = 0; h < 2; ++h) {
+      uint32_t t[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) t[j] = __float_as_uint(fmaf(v[4 * h + j], f, 12582912.f));
+      w[h] = __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
+    }
+  } else {  // the same for the whole quad
+    const uint32_t quad = 0xFu << (threadIdx.x & 28u);
+    uint32_t a = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a = max(a, act8_mag(v[j]));
+    a = max(a, __shfl_xor_sync(quad, a, 1));
+    a = max(a, __shfl_xor_sync(quad, a, 2));
+    b = act8_byte(a);
+    const Act8Scale s = act8_inv_scale(b);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      w[h] = act8_q(v[4 * h], s) | (act8_q(v[4 * h + 1], s) << 8) |
+             (act8_q(v[4 * h + 2], s) << 16) | (act8_q(v[4 * h + 3], s) << 24);
+  }
   q = make_uint2(w[0], w[1]);
   return b;
 }
 
+// The values of eight bytes.  Where 2^(b - 133) and 2^23 times it are normal
+// floats and no byte is -128, one FMA an element: (2^23 + 128 + q) s - (2^23 +
+// 128) s, both products exact.
 __device__ __forceinline__ void act8_unpack8(uint2 q, uint32_t b, float (&v)[8]) {
-  const Act8Scale s = act8_scale(b);
-  v[0] = act8_value<0>(q.x, s);
-  v[1] = act8_value<1>(q.x, s);
-  v[2] = act8_value<2>(q.x, s);
-  v[3] = act8_value<3>(q.x, s);
-  v[4] = act8_value<0>(q.y, s);
-  v[5] = act8_value<1>(q.y, s);
-  v[6] = act8_value<2>(q.y, s);
-  v[7] = act8_value<3>(q.y, s);
+  const uint32_t x = q.x ^ 0x80808080u, y = q.y ^ 0x80808080u;  // q + 128: 0 marks a NaN
+  const uint32_t nan = ((x - 0x01010101u) & ~x) | ((y - 0x01010101u) & ~y);
+  if (b >= 7u && b <= 228u && (nan & 0x80808080u) == 0u) {
+    const float s = pow2f(static_cast<int>(b) - 133), c = -8388736.f * s;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = fmaf(__uint_as_float(__byte_perm(x, 0x4B000000u, 0x7440 | j)), s, c);
+      v[4 + j] = fmaf(__uint_as_float(__byte_perm(y, 0x4B000000u, 0x7440 | j)), s, c);
+    }
+  } else {
+    const Act8Scale s = act8_scale(b);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = act8_value1(static_cast<int8_t>((q.x >> (8 * j)) & 0xFFu), s);
+      v[4 + j] = act8_value1(static_cast<int8_t>((q.y >> (8 * j)) & 0xFFu), s);
+    }
+  }
 }
 
 // ------------------------------------------------------------------- kernels
@@ -205,6 +251,8 @@ struct Act8Pos {
   }
 };
 
+constexpr int ACT8_UNROLL = 4;  // vectors a thread loads before it works on them
+
 template <typename TX, bool VEC>
 __global__ void __launch_bounds__(ACT8_THREADS)
 act8_pack_kernel(const TX* __restrict__ x, int64_t T, int32_t d, int32_t groups,
@@ -213,32 +261,50 @@ act8_pack_kernel(const TX* __restrict__ x, int64_t T, int32_t d, int32_t groups,
   const int sub = threadIdx.x % LANES;
   const int64_t tid = static_cast<int64_t>(blockIdx.x) * ACT8_THREADS + threadIdx.x;
   const int64_t nthr = static_cast<int64_t>(gridDim.x) * ACT8_THREADS;
-  const int64_t units = T * groups;
-  Act8Pos p(tid / LANES, nthr / LANES, groups);
+  const int64_t units = T * groups, step = nthr / LANES;
+  Act8Pos p(tid / LANES, step, groups);
   // whole warps take part in the group maxima: the loop runs while the
   // warp's first lane has a unit
-  for (int64_t u = (tid & ~int64_t(31)) / LANES; u < units; u += nthr / LANES, p.next(groups)) {
+  for (int64_t u = (tid & ~int64_t(31)) / LANES; u < units; u += ACT8_UNROLL * step) {
+    Act8Pos at[ACT8_UNROLL] = {p, p, p, p};
     if constexpr (VEC) {
-      const int32_t c = p.g * 32 + sub * 8;
-      const bool on = p.row < T && c < d;
-      Raw8<TX> r;
-      r.clear();
-      if (on) r.load(x + p.row * d + c);
-      float v[8];
-      r.get(v);
-      uint2 qq;
-      const uint32_t b = act8_pack8(v, qq);
-      if (on) {
-        *reinterpret_cast<uint2*>(q + p.row * d + c) = qq;
-        if (sub == 0) e[p.row * groups + p.g] = static_cast<uint8_t>(b);
+      Raw8<TX> r[ACT8_UNROLL];
+#pragma unroll
+      for (int k = 0; k < ACT8_UNROLL; ++k) {
+        at[k] = p;
+        p.next(groups);
+        r[k].clear();
+        if (at[k].row < T && at[k].g * 32 + sub * 8 < d)
+          r[k].load(x + at[k].row * d + at[k].g * 32 + sub * 8);
+      }
+#pragma unroll
+      for (int k = 0; k < ACT8_UNROLL; ++k) {
+        float v[8];
+        r[k].get(v);
+        uint2 qq;
+        const uint32_t b = act8_pack8(v, r[k].top(), qq);
+        if (at[k].row < T && at[k].g * 32 + sub * 8 < d) {
+          *reinterpret_cast<uint2*>(q + at[k].row * d + at[k].g * 32 + sub * 8) = qq;
+          if (sub == 0) e[at[k].row * groups + at[k].g] = static_cast<uint8_t>(b);
+        }
       }
     } else {
-      const int32_t c = p.g * 32 + sub;
-      const bool on = c < d;
-      const float v = on ? to_f32(x[p.row * d + c]) : 0.f;
-      const uint32_t b = act8_byte(__reduce_max_sync(0xffffffffu, act8_mag(v)));
-      if (on) q[p.row * d + c] = static_cast<int8_t>(act8_q(v, act8_inv_scale(b)));
-      if (sub == 0) e[p.row * groups + p.g] = static_cast<uint8_t>(b);
+      float v[ACT8_UNROLL];
+#pragma unroll
+      for (int k = 0; k < ACT8_UNROLL; ++k) {
+        at[k] = p;
+        p.next(groups);
+        const int32_t c = at[k].g * 32 + sub;
+        v[k] = at[k].row < T && c < d ? to_f32(x[at[k].row * d + c]) : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < ACT8_UNROLL; ++k) {
+        const int32_t c = at[k].g * 32 + sub;
+        const uint32_t b = act8_byte(__reduce_max_sync(0xffffffffu, act8_mag(v[k])));
+        if (at[k].row >= T) continue;
+        if (c < d) q[at[k].row * d + c] = static_cast<int8_t>(act8_q(v[k], act8_inv_scale(b)));
+        if (sub == 0) e[at[k].row * groups + at[k].g] = static_cast<uint8_t>(b);
+      }
     }
   }
 }
@@ -248,26 +314,38 @@ __global__ void __launch_bounds__(ACT8_THREADS)
 act8_unpack_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ e, int64_t T,
                    int32_t d, int32_t groups, TX* __restrict__ x) {
   constexpr int LANES = VEC ? 4 : 32;
+  using Q = typename std::conditional<VEC, uint2, int8_t>::type;
   const int sub = threadIdx.x % LANES;
   const int64_t tid = static_cast<int64_t>(blockIdx.x) * ACT8_THREADS + threadIdx.x;
   const int64_t nthr = static_cast<int64_t>(gridDim.x) * ACT8_THREADS;
-  const int64_t units = T * groups;
-  Act8Pos p(tid / LANES, nthr / LANES, groups);
-  for (int64_t u = tid / LANES; u < units; u += nthr / LANES, p.next(groups)) {
-    if constexpr (VEC) {
-      const int32_t c = p.g * 32 + sub * 8;
-      if (c >= d) continue;
-      float v[8];
-      act8_unpack8(*reinterpret_cast<const uint2*>(q + p.row * d + c),
-                   e[p.row * groups + p.g], v);
-      Raw8<TX> r;
-      r.set(v);
-      r.store(x + p.row * d + c);
-    } else {
-      const int32_t c = p.g * 32 + sub;
-      if (c < d)
-        x[p.row * d + c] =
-            from_f32<TX>(act8_value1(q[p.row * d + c], act8_scale(e[p.row * groups + p.g])));
+  const int64_t units = T * groups, step = nthr / LANES;
+  Act8Pos p(tid / LANES, step, groups);
+  for (int64_t u = tid / LANES; u < units; u += ACT8_UNROLL * step) {
+    Q qq[ACT8_UNROLL];
+    uint32_t b[ACT8_UNROLL];
+    int64_t at[ACT8_UNROLL];  // first element, -1: none
+#pragma unroll
+    for (int k = 0; k < ACT8_UNROLL; ++k) {
+      const int32_t c = p.g * 32 + sub * (VEC ? 8 : 1);
+      at[k] = p.row < T && c < d ? p.row * d + c : -1;
+      if (at[k] >= 0) {
+        qq[k] = *reinterpret_cast<const Q*>(q + at[k]);
+        b[k] = e[p.row * groups + p.g];
+      }
+      p.next(groups);
+    }
+#pragma unroll
+    for (int k = 0; k < ACT8_UNROLL; ++k) {
+      if (at[k] < 0) continue;
+      if constexpr (VEC) {
+        float v[8];
+        act8_unpack8(qq[k], b[k], v);
+        Raw8<TX> r;
+        r.set(v);
+        r.store(x + at[k]);
+      } else {
+        x[at[k]] = from_f32<TX>(act8_value1(qq[k], act8_scale(b[k])));
+      }
     }
   }
 }

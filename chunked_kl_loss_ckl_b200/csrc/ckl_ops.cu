@@ -12,8 +12,7 @@
 #include "ckl_norm.cuh"
 #include "ckl_sample.cuh"
 
-static_assert(CKL_ACT8_GROUP == ckl::ACT8_GROUP && CKL_NORM_MAX_D == ckl::NORM_MAX_D &&
-                  CKL_SAMPLE_BAD_INPUT == CKL_DEV_BAD_SAMPLE,
+static_assert(CKL_ACT8_GROUP == ckl::ACT8_GROUP && CKL_SAMPLE_BAD_INPUT == CKL_DEV_BAD_SAMPLE,
               "the header's constants");
 
 namespace {
@@ -80,47 +79,108 @@ void act8_unpack_launch(const int8_t* q, const uint8_t* e, int64_t T, int64_t d,
                                         static_cast<int32_t>(groups), static_cast<TX*>(x));
 }
 
-// Threads of a row and vectors a thread: the fewest vectors a thread for which
-// a row fits in 1024 threads, whole warps.
+// How a norm's rows are taken: `vec` elements a load, `nv` vectors a thread,
+// `tpr` threads a row, `threads` a block; nv 0 = the kernels for long rows.
 struct NormShape {
-  int vec, nv, tpr, rpb;
+  int vec, nv, tpr, threads;
 };
-NormShape norm_shape(int64_t d, bool vec) {
-  NormShape s;
-  s.vec = vec ? 8 : 1;
+
+// Two vectors a thread where a row has more than 1024 elements: half as many
+// warps to join per row.  Element-wise rows take eight elements a thread.
+// max_nv: the most vectors a thread's registers and its ring hold.
+NormShape norm_shape(int64_t d, bool vec, int max_nv) {
+  NormShape s{vec ? 8 : 1, 0, 0, 0};
   const int64_t n = cdiv(d, s.vec);  // vectors of a row
-  s.nv = vec ? (n <= 1024 ? 1 : n <= 2048 ? 2 : 4) : (n <= 8192 ? 8 : 32);
+  const int cand_vec[] = {1, 2, 4}, cand_one[] = {8, 16};
+  const int* cand = vec ? cand_vec : cand_one;
+  const int count = vec ? 3 : 2;
+  for (int i = 0; i < count && cand[i] <= max_nv; ++i) {
+    if (vec && cand[i] == 1 && n > 128) continue;
+    if (n <= static_cast<int64_t>(ckl::NORM_THREADS) * cand[i]) {
+      s.nv = cand[i];
+      break;
+    }
+  }
+  if (s.nv == 0) return s;
   s.tpr = static_cast<int>(cdiv(cdiv(n, s.nv), 32) * 32);
-  s.rpb = std::max(1, 128 / s.tpr);  // blocks of at least four warps
+  s.threads = ckl::NORM_THREADS / s.tpr * s.tpr;
   return s;
 }
 
+template <typename P>
+int norm_launch(void (*k)(P), const P& p, dim3 grid, int threads, size_t smem, cudaStream_t st) {
+  // 48 KB, the kernel's static part included, need no opting in
+  if (smem > 40 * 1024 &&
+      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem)) != cudaSuccess)
+    return CKL_ERR_CUDA;
+  k<<<grid, threads, smem, st>>>(p);
+  return launched();
+}
+
 template <typename TX>
-void norm_fwd_launch(const ckl::NormFwd& p, const NormShape& s, unsigned grid, cudaStream_t st) {
-  void (*k)(ckl::NormFwd) = nullptr;
+int norm_fwd_launch(const ckl::NormFwd& p, const NormShape& s, int sms, cudaStream_t st) {
+  using ckl::NORM_FWD_BYTES;
+  using ckl::norm_stages;
+  const int64_t rows = std::min<int64_t>(p.T, static_cast<int64_t>(sms) * 4);
+  if (s.nv == 0)
+    return norm_launch(s.vec == 8 ? ckl::norm_fwd_long_kernel<TX, 8>
+                                  : ckl::norm_fwd_long_kernel<TX, 1>,
+                       p, dim3(static_cast<unsigned>(rows)), ckl::NORM_THREADS, 0, st);
+  // two blocks an SM (one with four vectors a thread), every row group a row
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(p.T, sms * (s.nv == 4 ? 1 : 2))));
+  auto go = [&](void (*k)(ckl::NormFwd), int bytes) {
+    return norm_launch(k, p, grid, s.threads,
+                       static_cast<size_t>(s.threads) * bytes * norm_stages(bytes), st);
+  };
   if (s.vec == 8)
-    k = s.nv == 1 ? ckl::norm_fwd_kernel<TX, 8, 1>
-        : s.nv == 2 ? ckl::norm_fwd_kernel<TX, 8, 2> : ckl::norm_fwd_kernel<TX, 8, 4>;
-  else
-    k = s.nv == 8 ? ckl::norm_fwd_kernel<TX, 1, 8> : ckl::norm_fwd_kernel<TX, 1, 32>;
-  k<<<grid, s.tpr * s.rpb, 0, st>>>(p);
+    return s.nv == 1   ? go(ckl::norm_fwd_kernel<TX, 8, 1>, NORM_FWD_BYTES<TX, 1>)
+           : s.nv == 2 ? go(ckl::norm_fwd_kernel<TX, 8, 2>, NORM_FWD_BYTES<TX, 2>)
+                       : go(ckl::norm_fwd_kernel<TX, 8, 4>, NORM_FWD_BYTES<TX, 4>);
+  return norm_launch(s.nv == 8 ? ckl::norm_fwd_kernel<TX, 1, 8> : ckl::norm_fwd_kernel<TX, 1, 16>,
+                     p, grid, s.threads, 0, st);
 }
 
+// Returns the status; `parts` is how many sums the workspace then holds.
 template <typename TX, bool Q8>
-void norm_bwd_launch(const ckl::NormBwd& p, const NormShape& s, unsigned grid, cudaStream_t st) {
-  void (*k)(ckl::NormBwd) = nullptr;
-  if (s.vec == 8)
-    k = s.nv == 1 ? ckl::norm_bwd_kernel<TX, 8, 1, Q8>
-        : s.nv == 2 ? ckl::norm_bwd_kernel<TX, 8, 2, Q8> : ckl::norm_bwd_kernel<TX, 8, 4, Q8>;
-  else
-    k = s.nv == 8 ? ckl::norm_bwd_kernel<TX, 1, 8, Q8> : ckl::norm_bwd_kernel<TX, 1, 32, Q8>;
-  k<<<grid, s.tpr * s.rpb, 0, st>>>(p);
+int norm_bwd_launch(const ckl::NormBwd& p, const NormShape& s, int sms, cudaStream_t st,
+                    int& parts) {
+  using ckl::NORM_BWD_BYTES;
+  using ckl::norm_stages;
+  if (s.nv == 0) {
+    parts = static_cast<int>(std::min<int64_t>(cdiv(p.T, 8 * ckl::NORM_COL_WARPS), 64));
+    if (p.want_gamma || p.want_beta) {  // first: dx may take dy's place
+      const dim3 grid(static_cast<unsigned>(cdiv(p.d, 32 * s.vec)), static_cast<unsigned>(parts));
+      const int rc = norm_launch(s.vec == 8 ? ckl::norm_cols_kernel<TX, 8, Q8>
+                                            : ckl::norm_cols_kernel<TX, 1, Q8>,
+                                 p, grid, 32 * ckl::NORM_COL_WARPS, 0, st);
+      if (rc != CKL_OK) return rc;
+    }
+    return norm_launch(s.vec == 8 ? ckl::norm_bwd_long_kernel<TX, 8, Q8>
+                                  : ckl::norm_bwd_long_kernel<TX, 1, Q8>,
+                       p, dim3(static_cast<unsigned>(std::min<int64_t>(p.T, sms * 4))),
+                       ckl::NORM_THREADS, 0, st);
+  }
+  parts = static_cast<int>(std::min<int64_t>(p.T, std::min(sms, ckl::NORM_MAX_PARTS)));
+  const dim3 grid(static_cast<unsigned>(parts));
+  const size_t sums = static_cast<size_t>(p.d) * 8;  // a row group's, on the way to the first's
+  auto go = [&](void (*k)(ckl::NormBwd), int bytes) {
+    const size_t ring = static_cast<size_t>(s.threads) * bytes * norm_stages(bytes);
+    return norm_launch(k, p, grid, s.threads, std::max(ring, sums), st);
+  };
+  if (s.vec == 8) {
+    if constexpr (sizeof(TX) == 2)
+      if (s.nv == 4) return go(ckl::norm_bwd_kernel<TX, 8, 4, Q8>, NORM_BWD_BYTES<TX, 4, Q8>);
+    return s.nv == 1 ? go(ckl::norm_bwd_kernel<TX, 8, 1, Q8>, NORM_BWD_BYTES<TX, 1, Q8>)
+                     : go(ckl::norm_bwd_kernel<TX, 8, 2, Q8>, NORM_BWD_BYTES<TX, 2, Q8>);
+  }
+  return norm_launch(s.nv == 8 ? ckl::norm_bwd_kernel<TX, 1, 8, Q8>
+                               : ckl::norm_bwd_kernel<TX, 1, 16, Q8>,
+                     p, grid, s.threads, sums, st);
 }
 
-// CKL_OK, or what is wrong with a norm's sizes.
-int norm_sizes(int64_t T, int64_t d) {
-  if (T < 0 || d < 1 || T >= (int64_t(1) << 40)) return CKL_ERR_INVALID_ARG;
-  return d > ckl::NORM_MAX_D ? CKL_ERR_UNSUPPORTED : CKL_OK;
+bool norm_sizes_ok(int64_t T, int64_t d) {
+  return T >= 0 && d >= 1 && d < kLim - 65536 && T < (int64_t(1) << 60) / d;
 }
 
 }  // namespace
@@ -166,7 +226,7 @@ int ckl_norm_forward(const void* x, int32_t dtype, const void* gamma, const void
                      float* rstd, int8_t* q, uint8_t* exponents, void* stream) {
   if (!dtype_ok(dtype) || !dtype_ok(param_dtype) || !(eps >= 0.f) || std::isinf(eps))
     return CKL_ERR_INVALID_ARG;
-  if (const int rc = norm_sizes(T, d)) return rc;
+  if (!norm_sizes_ok(T, d)) return CKL_ERR_INVALID_ARG;
   if (T > 0 && (!x || !y || !rstd)) return CKL_ERR_INVALID_ARG;
   if ((q == nullptr) != (exponents == nullptr)) return CKL_ERR_INVALID_ARG;
   const size_t eb = elem_bytes(dtype), pb = elem_bytes(param_dtype);
@@ -178,7 +238,7 @@ int ckl_norm_forward(const void* x, int32_t dtype, const void* gamma, const void
   if (T == 0) return CKL_OK;
   const bool vec = d % 8 == 0 && aligned(x, 16) && aligned(y, 16) && aligned(gamma, 16) &&
                    aligned(beta, 16) && aligned(q, 8);
-  const NormShape s = norm_shape(d, vec);
+  const NormShape s = norm_shape(d, vec, vec ? 4 : 16);
   ckl::NormFwd p{};
   p.x = x;
   p.gamma = gamma;
@@ -194,16 +254,13 @@ int ckl_norm_forward(const void* x, int32_t dtype, const void* gamma, const void
   p.tpr = s.tpr;
   p.param_f32 = param_dtype == CKL_DTYPE_F32;
   p.eps = eps;
-  const unsigned grid = static_cast<unsigned>(
-      std::min<int64_t>(cdiv(T, s.rpb), static_cast<int64_t>(dev.sms) * 16));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (dtype == CKL_DTYPE_F32) norm_fwd_launch<float>(p, s, grid, st);
-  else norm_fwd_launch<bf16>(p, s, grid, st);
-  return launched();
+  return dtype == CKL_DTYPE_F32 ? norm_fwd_launch<float>(p, s, dev.sms, st)
+                                : norm_fwd_launch<bf16>(p, s, dev.sms, st);
 }
 
 size_t ckl_norm_workspace_bytes(int64_t T, int64_t d) {
-  if (norm_sizes(T, d) != CKL_OK) return 0;
+  if (!norm_sizes_ok(T, d)) return 0;
   const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(T, ckl::NORM_MAX_PARTS));
   return static_cast<size_t>(parts) * 2 * d * 4;
 }
@@ -214,7 +271,7 @@ int ckl_norm_backward(const void* dy, int32_t dtype, const void* x, const int8_t
                       float* dgamma, float* dbeta, int32_t accumulate, void* workspace,
                       size_t workspace_bytes, void* stream) {
   if (!dtype_ok(dtype) || !dtype_ok(param_dtype)) return CKL_ERR_INVALID_ARG;
-  if (const int rc = norm_sizes(T, d)) return rc;
+  if (!norm_sizes_ok(T, d)) return CKL_ERR_INVALID_ARG;
   if (T > 0 && (!dy || !dx || !rstd)) return CKL_ERR_INVALID_ARG;
   if (T > 0 && !x && (!q || !exponents)) return CKL_ERR_INVALID_ARG;
   const bool grads = dgamma || dbeta;
@@ -231,10 +288,7 @@ int ckl_norm_backward(const void* dy, int32_t dtype, const void* x, const int8_t
   const bool q8 = x == nullptr;
   const bool vec = d % 8 == 0 && aligned(dy, 16) && aligned(x, 16) && aligned(dx, 16) &&
                    aligned(gamma, 16) && (!q8 || aligned(q, 8));
-  const NormShape s = norm_shape(d, vec);
-  // one part of the gradients' sums for every row group of the launch
-  const int64_t blocks = std::min<int64_t>(
-      cdiv(T, s.rpb), std::min<int64_t>(dev.sms * 2, ckl::NORM_MAX_PARTS / s.rpb));
+  const NormShape s = norm_shape(d, vec, !vec ? 16 : dtype == CKL_DTYPE_F32 ? 2 : 4);
   int parts = 0;
   if (T > 0) {
     ckl::NormBwd p{};
@@ -254,25 +308,29 @@ int ckl_norm_backward(const void* dy, int32_t dtype, const void* x, const int8_t
     p.param_f32 = param_dtype == CKL_DTYPE_F32;
     p.want_gamma = dgamma != nullptr;
     p.want_beta = dbeta != nullptr;
-    parts = static_cast<int>(std::min<int64_t>(blocks * s.rpb, T));
-    const unsigned grid = static_cast<unsigned>(blocks);
-    if (dtype == CKL_DTYPE_F32) {
-      if (q8) norm_bwd_launch<float, true>(p, s, grid, st);
-      else norm_bwd_launch<float, false>(p, s, grid, st);
-    } else {
-      if (q8) norm_bwd_launch<bf16, true>(p, s, grid, st);
-      else norm_bwd_launch<bf16, false>(p, s, grid, st);
-    }
-    if (launched() != CKL_OK) return CKL_ERR_CUDA;
+    const int rc =
+        dtype == CKL_DTYPE_F32
+            ? (q8 ? norm_bwd_launch<float, true>(p, s, dev.sms, st, parts)
+                  : norm_bwd_launch<float, false>(p, s, dev.sms, st, parts))
+            : (q8 ? norm_bwd_launch<bf16, true>(p, s, dev.sms, st, parts)
+                  : norm_bwd_launch<bf16, false>(p, s, dev.sms, st, parts));
+    if (rc != CKL_OK) return rc;
   }
-  if (grads) {
-    const dim3 grid(static_cast<unsigned>(cdiv(d, ckl::NORM_RED_COLS)), 2);
-    ckl::norm_reduce_kernel<<<grid, ckl::NORM_RED_COLS * ckl::NORM_RED_ROWS, 0, st>>>(
-        static_cast<const float*>(workspace), parts, static_cast<int32_t>(d), dgamma, dbeta,
-        accumulate);
-    return launched();
-  }
-  return CKL_OK;
+  if (!grads) return CKL_OK;
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(cdiv(d, ckl::NORM_RED_COLS)), 2);
+  cfg.blockDim = dim3(ckl::NORM_RED_COLS * ckl::NORM_RED_ROWS);
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, ckl::norm_reduce_kernel, static_cast<const float*>(workspace),
+                            parts, static_cast<int32_t>(d), dgamma, dbeta, accumulate) ==
+                 cudaSuccess
+             ? CKL_OK
+             : CKL_ERR_CUDA;
 }
 
 int ckl_sample(const uint16_t* logits, int64_t ld, int64_t T, int64_t V, const float* u, int32_t N,

@@ -27,8 +27,6 @@ enum {
 
 /* Elements of a row that share a scale in the 8-bit form. */
 #define CKL_ACT8_GROUP 32
-/* Longest row of the norm. */
-#define CKL_NORM_MAX_D 32768
 /* Largest vocabulary of ckl_sample. */
 #define CKL_SAMPLE_MAX_V 4194304
 /* Bit of ckl_sample's device_status: a NaN or +inf logit, or a row's parameter
@@ -66,8 +64,7 @@ CKL_API int ckl_act8_unpack(const int8_t* q, const uint8_t* exponents, int64_t T
  *   mean, rstd [T] fp32  out: mu and r, for the backward; mean may be NULL
  *   q, exponents         out: x in 8 bits, for a backward that does not keep
  *                        x (ckl_act8_pack's result); both NULL = none
- * T >= 0, 1 <= d <= CKL_NORM_MAX_D (CKL_ERR_UNSUPPORTED above), eps >= 0 and
- * finite.  Arrays aligned to their elements; rows are taken 16 bytes at a time when
+ * T >= 0, 1 <= d < 2^31 - 2^17, T d < 2^60, eps >= 0 and finite.  Arrays aligned to their elements; rows are taken 16 bytes at a time when
  * d % 8 == 0, x, y, gamma and beta are 16-byte and q 8-byte aligned.  y may be x.
  */
 CKL_API int ckl_norm_forward(const void* x, int32_t dtype, const void* gamma, const void* beta,

@@ -23,7 +23,7 @@ BF, F32 = torch.bfloat16, torch.float32
 # the widths at which the kernels change (warps a row, vectors a thread, whole
 # vectors or single elements), and some between
 WIDTHS = [1, 7, 8, 31, 32, 33, 40, 256, 264, 1001, 1024, 2880, 4096, 8192, 8200, 8201, 16384,
-          16400, 32767, 32768]
+          16400, 32767, 32768, 100003]
 
 
 def _make(T, d, dtype, seed=0, pdtype=None, offset=0.3):
@@ -112,7 +112,7 @@ def test_forward_and_backward_at_every_width(gpu_lib, d, dtype):
 
 
 @pytest.mark.parametrize("T,d", [(1, 4096), (149, 2880), (1500, 64), (5000, 8), (3000, 1001),
-                                 (700, 4096), (640, 16384)])
+                                 (700, 4096), (640, 16384), (300, 20000), (300, 9001)])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_many_rows(gpu_lib, T, d, dtype):
     x, gamma, beta, dy = _make(T, d, dtype, seed=1)
@@ -365,7 +365,7 @@ def test_refusals(gpu_lib):
     with pytest.raises(TypeError):
         gpu_lib.norm_forward(x, gamma, beta.float())
     with pytest.raises(gpu_lib.CklError):
-        gpu_lib.norm_forward(torch.zeros(1, 32769, dtype=BF, device="cuda"))
+        gpu_lib.norm_forward(x, gamma, eps=-1.0)
     with pytest.raises(TypeError):
         gpu_lib.norm_backward(dy, x.float(), mean, rstd, gamma)
     with pytest.raises(ValueError):
