@@ -22,6 +22,8 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "ckl_bf16.cuh"
+
 namespace ckl {
 
 constexpr int ACT8_GROUP = 32;
@@ -86,16 +88,47 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
   return __float2bfloat16_rn(x);
 }
 
-// Largest magnitude bits of eight elements, non-finite ones included.
-__device__ __forceinline__ uint32_t act8_top8(const float (&v)[8]) {
-  uint32_t a = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) a = max(a, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-  return a;
+// VEC elements of a row in registers: eight as four packed pairs of fp32 (for
+// the two-lane instructions, which halve what a row costs to issue), or one.
+template <int VEC>
+struct Lane;
+template <>
+struct Lane<8> {
+  static constexpr int N = 4;
+  using E = uint64_t;
+  E e[N];
+  __device__ __forceinline__ float get(int j) const {
+    return (j & 1) ? f32x2_hi(e[j / 2]) : f32x2_lo(e[j / 2]);
+  }
+};
+template <>
+struct Lane<1> {
+  static constexpr int N = 1;
+  using E = float;
+  E e[N];
+  __device__ __forceinline__ float get(int) const { return e[0]; }
+};
+template <typename E>
+__device__ __forceinline__ E both(float x);
+template <>
+__device__ __forceinline__ float both<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ uint64_t both<uint64_t>(float x) { return f32x2_pack(x, x); }
+__device__ __forceinline__ float vadd(float a, float b) { return a + b; }
+__device__ __forceinline__ uint64_t vadd(uint64_t a, uint64_t b) { return f32x2_add(a, b); }
+__device__ __forceinline__ float vsub(float a, float b) { return a - b; }
+__device__ __forceinline__ uint64_t vsub(uint64_t a, uint64_t b) { return f32x2_sub(a, b); }
+__device__ __forceinline__ float vmul(float a, float b) { return a * b; }
+__device__ __forceinline__ uint64_t vmul(uint64_t a, uint64_t b) { return f32x2_mul(a, b); }
+__device__ __forceinline__ float vfma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ uint64_t vfma(uint64_t a, uint64_t b, uint64_t c) {
+  return f32x2_fma(a, b, c);
 }
+__device__ __forceinline__ float vsum(float a) { return a; }
+__device__ __forceinline__ float vsum(uint64_t a) { return f32x2_lo(a) + f32x2_hi(a); }
 
-// Eight consecutive elements as loaded: one 16-byte vector of bf16 or two of
-// float.
+// Eight consecutive elements as they are in memory: one 16-byte piece of bf16
+// or two of float.
 template <typename T>
 struct Raw8;
 template <>
@@ -104,7 +137,7 @@ struct Raw8<__nv_bfloat16> {
   __device__ __forceinline__ void load(const __nv_bfloat16* p) {
     a = *reinterpret_cast<const uint4*>(p);
   }
-  // its 16-byte pieces, `piece` bytes apart
+  // its pieces, `piece` bytes apart
   __device__ __forceinline__ void load_pieces(const uint8_t* p, uint32_t) {
     a = *reinterpret_cast<const uint4*>(p);
   }
@@ -115,19 +148,17 @@ struct Raw8<__nv_bfloat16> {
     const uint32_t m = __vmaxu2(__vmaxu2(a.x & k, a.y & k), __vmaxu2(a.z & k, a.w & k));
     return max(m & 0xFFFF0000u, m << 16);
   }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = __uint_as_float(w[j] << 16);
-      v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-    }
+  __device__ __forceinline__ void get(Lane<8>& v) const {
+    v.e[0] = bf16x2_widen(a.x);
+    v.e[1] = bf16x2_widen(a.y);
+    v.e[2] = bf16x2_widen(a.z);
+    v.e[3] = bf16x2_widen(a.w);
   }
-  __device__ __forceinline__ void set(const float (&v)[8]) {
+  __device__ __forceinline__ void set(const Lane<8>& v) {
     uint32_t w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+      const __nv_bfloat162 p = __floats2bfloat162_rn(f32x2_lo(v.e[j]), f32x2_hi(v.e[j]));
       w[j] = *reinterpret_cast<const uint32_t*>(&p);
     }
     a = make_uint4(w[0], w[1], w[2], w[3]);
@@ -138,41 +169,48 @@ struct Raw8<__nv_bfloat16> {
 };
 template <>
 struct Raw8<float> {
-  float4 a, b;
+  ulonglong2 a, b;
   __device__ __forceinline__ void load(const float* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
+    a = reinterpret_cast<const ulonglong2*>(p)[0];
+    b = reinterpret_cast<const ulonglong2*>(p)[1];
   }
   __device__ __forceinline__ void load_pieces(const uint8_t* p, uint32_t piece) {
-    a = *reinterpret_cast<const float4*>(p);
-    b = *reinterpret_cast<const float4*>(p + piece);
+    a = *reinterpret_cast<const ulonglong2*>(p);
+    b = *reinterpret_cast<const ulonglong2*>(p + piece);
   }
-  __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void clear() { a = b = make_ulonglong2(0ull, 0ull); }
   __device__ __forceinline__ uint32_t top() const {
-    float v[8];
-    get(v);
-    return act8_top8(v);
+    const uint64_t k = 0x7FFFFFFF7FFFFFFFull;
+    const uint64_t w[4] = {a.x & k, a.y & k, b.x & k, b.y & k};
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      m = max(m, max(static_cast<uint32_t>(w[j]), static_cast<uint32_t>(w[j] >> 32)));
+    return m;
   }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  __device__ __forceinline__ void get(Lane<8>& v) const {
+    v.e[0] = a.x;
+    v.e[1] = a.y;
+    v.e[2] = b.x;
+    v.e[3] = b.y;
   }
-  __device__ __forceinline__ void set(const float (&v)[8]) {
-    a = make_float4(v[0], v[1], v[2], v[3]);
-    b = make_float4(v[4], v[5], v[6], v[7]);
+  __device__ __forceinline__ void set(const Lane<8>& v) {
+    a = make_ulonglong2(v.e[0], v.e[1]);
+    b = make_ulonglong2(v.e[2], v.e[3]);
   }
   __device__ __forceinline__ void store(float* p) const {
-    reinterpret_cast<float4*>(p)[0] = a;
-    reinterpret_cast<float4*>(p)[1] = b;
+    reinterpret_cast<ulonglong2*>(p)[0] = a;
+    reinterpret_cast<ulonglong2*>(p)[1] = b;
   }
 };
 
 // Eight elements of one lane to 8 bits; the four lanes of an aligned quad hold
-// one group of 32.  `top` is act8_top8(v).  Returns the exponent byte; q is the
-// eight bytes.  Where the group is finite and both 2^(133 - b) and the sums
-// below are normal floats, one FMA scales and rounds an element:
-// v 2^(133 - b) + 1.5 2^23 has the integer in its low byte.
-__device__ __forceinline__ uint32_t act8_pack8(const float (&v)[8], uint32_t top, uint2& q) {
+// one group of 32 (whole quads call it).  `top` is the lane's Raw8::top().
+// Returns the exponent byte; q is the eight bytes.  Where the group is finite
+// and both 2^(133 - b) and the sums below are normal floats, one FMA scales
+// and rounds an element: v 2^(133 - b) + 1.5 2^23 has the integer in its low
+// byte.
+__device__ __forceinline__ uint32_t act8_pack8(const Lane<8>& v, uint32_t top, uint2& q) {
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
   uint32_t b = act8_byte(top);
@@ -181,24 +219,25 @@ __device__ __forceinline__ uint32_t act8_pack8(const float (&v)[8], uint32_t top
     const float f = pow2f(133 - static_cast<int>(b));
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint32_t t[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) t[j] = __float_as_uint(fmaf(v[4 * h + j], f, 12582912.f));
-      w[h] = __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
+      const uint64_t s = f32x2_fma(v.e[2 * h], both<uint64_t>(f), both<uint64_t>(12582912.f));
+      const uint64_t t = f32x2_fma(v.e[2 * h + 1], both<uint64_t>(f), both<uint64_t>(12582912.f));
+      w[h] = __byte_perm(
+          __byte_perm(static_cast<uint32_t>(s), static_cast<uint32_t>(s >> 32), 0x0040),
+          __byte_perm(static_cast<uint32_t>(t), static_cast<uint32_t>(t >> 32), 0x0040), 0x5410);
     }
   } else {  // the same for the whole quad
     const uint32_t quad = 0xFu << (threadIdx.x & 28u);
     uint32_t a = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) a = max(a, act8_mag(v[j]));
+    for (int j = 0; j < 8; ++j) a = max(a, act8_mag(v.get(j)));
     a = max(a, __shfl_xor_sync(quad, a, 1));
     a = max(a, __shfl_xor_sync(quad, a, 2));
     b = act8_byte(a);
     const Act8Scale s = act8_inv_scale(b);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      w[h] = act8_q(v[4 * h], s) | (act8_q(v[4 * h + 1], s) << 8) |
-             (act8_q(v[4 * h + 2], s) << 16) | (act8_q(v[4 * h + 3], s) << 24);
+      w[h] = act8_q(v.get(4 * h), s) | (act8_q(v.get(4 * h + 1), s) << 8) |
+             (act8_q(v.get(4 * h + 2), s) << 16) | (act8_q(v.get(4 * h + 3), s) << 24);
   }
   q = make_uint2(w[0], w[1]);
   return b;
@@ -207,22 +246,28 @@ __device__ __forceinline__ uint32_t act8_pack8(const float (&v)[8], uint32_t top
 // The values of eight bytes.  Where 2^(b - 133) and 2^23 times it are normal
 // floats and no byte is -128, one FMA an element: (2^23 + 128 + q) s - (2^23 +
 // 128) s, both products exact.
-__device__ __forceinline__ void act8_unpack8(uint2 q, uint32_t b, float (&v)[8]) {
+__device__ __forceinline__ void act8_unpack8(uint2 q, uint32_t b, Lane<8>& v) {
   const uint32_t x = q.x ^ 0x80808080u, y = q.y ^ 0x80808080u;  // q + 128: 0 marks a NaN
   const uint32_t nan = ((x - 0x01010101u) & ~x) | ((y - 0x01010101u) & ~y);
   if (b >= 7u && b <= 228u && (nan & 0x80808080u) == 0u) {
-    const float s = pow2f(static_cast<int>(b) - 133), c = -8388736.f * s;
+    const float s = pow2f(static_cast<int>(b) - 133);
+    const uint64_t s2 = both<uint64_t>(s), c2 = both<uint64_t>(-8388736.f * s);
+    const uint32_t k = 0x4B000000u;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[j] = fmaf(__uint_as_float(__byte_perm(x, 0x4B000000u, 0x7440 | j)), s, c);
-      v[4 + j] = fmaf(__uint_as_float(__byte_perm(y, 0x4B000000u, 0x7440 | j)), s, c);
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t w = h ? y : x;
+      v.e[2 * h] = f32x2_fma(f32x2_pack(__uint_as_float(__byte_perm(w, k, 0x7440)),
+                                        __uint_as_float(__byte_perm(w, k, 0x7441))), s2, c2);
+      v.e[2 * h + 1] = f32x2_fma(f32x2_pack(__uint_as_float(__byte_perm(w, k, 0x7442)),
+                                            __uint_as_float(__byte_perm(w, k, 0x7443))), s2, c2);
     }
   } else {
     const Act8Scale s = act8_scale(b);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      v[j] = act8_value1(static_cast<int8_t>((q.x >> (8 * j)) & 0xFFu), s);
-      v[4 + j] = act8_value1(static_cast<int8_t>((q.y >> (8 * j)) & 0xFFu), s);
+      const uint32_t w = (j < 2 ? q.x : q.y) >> (16 * (j & 1));
+      v.e[j] = f32x2_pack(act8_value1(static_cast<int8_t>(w & 0xFFu), s),
+                          act8_value1(static_cast<int8_t>((w >> 8) & 0xFFu), s));
     }
   }
 }
@@ -279,7 +324,7 @@ act8_pack_kernel(const TX* __restrict__ x, int64_t T, int32_t d, int32_t groups,
       }
 #pragma unroll
       for (int k = 0; k < ACT8_UNROLL; ++k) {
-        float v[8];
+        Lane<8> v;
         r[k].get(v);
         uint2 qq;
         const uint32_t b = act8_pack8(v, r[k].top(), qq);
@@ -338,7 +383,7 @@ act8_unpack_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ e, 
     for (int k = 0; k < ACT8_UNROLL; ++k) {
       if (at[k] < 0) continue;
       if constexpr (VEC) {
-        float v[8];
+        Lane<8> v;
         act8_unpack8(qq[k], b[k], v);
         Raw8<TX> r;
         r.set(v);

@@ -48,7 +48,7 @@ struct NormFwd {
   int8_t* q;  // null: no 8-bit copy of x
   uint8_t* e;
   int64_t T;
-  int32_t d, groups, tpr, param_f32;
+  int32_t d, groups, tpr, param_f32, staged;  // staged: the parameters go to shared memory
   float eps;
 };
 
@@ -63,7 +63,7 @@ struct NormBwd {
   void* dx;
   float* parts;  // [parts, 2, d]: sums of dgamma and dbeta
   int64_t T;
-  int32_t d, groups, tpr, param_f32, want_gamma, want_beta;
+  int32_t d, groups, tpr, param_f32, staged, want_gamma, want_beta;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -90,88 +90,103 @@ constexpr int NORM_FWD_BYTES = NV * 8 * static_cast<int>(sizeof(TX));
 template <typename TX, int NV, bool Q8>
 constexpr int NORM_BWD_BYTES = NV * 8 * (static_cast<int>(sizeof(TX)) * (Q8 ? 1 : 2) + (Q8 ? 1 : 0));
 
-__device__ __forceinline__ float2 warp_sum2(float a, float b) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, o);
-    b += __shfl_xor_sync(0xffffffffu, b, o);
-  }
-  return make_float2(a, b);
-}
-
 // What the warps of a row's group tell each other through shared memory.  Two
-// buffers take turns, so that one barrier an exchange is enough.
+// buffers take turns, so that one barrier an exchange is enough.  Warp w's two
+// numbers are at [0][w] and [1][w]; lanes 0-15 and 16-31 read one of the two
+// each and add them up in a butterfly, so that the sums cost the same few
+// instructions however many warps a row has.
 struct RowGroup {
-  float2 (*red)[32];
-  int buf, warp0, warps, bar, tpr;
-  __device__ __forceinline__ RowGroup(float2 (*r)[32], int tpr_)
-      : red(r), buf(0), warp0((threadIdx.x / tpr_) * (tpr_ / 32)), warps(tpr_ / 32),
-        bar(1 + threadIdx.x / tpr_), tpr(tpr_) {}
-  __device__ __forceinline__ const float2* exchange(float2 mine) {
-    if ((threadIdx.x & 31) == 0) red[buf][threadIdx.x >> 5] = mine;
-    asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(tpr) : "memory");
-    const float2* all = &red[buf][warp0];
-    buf ^= 1;
-    return all;
+  float (*red)[2][16];
+  int buf, warp0, warps, half, bar, tpr;
+  __device__ __forceinline__ RowGroup(float (*r)[2][16], int tpr_)
+      : red(r), buf(0), warp0((threadIdx.x / tpr_) * (tpr_ / 32)), warps(tpr_ / 32), half(1),
+        bar(1 + threadIdx.x / tpr_), tpr(tpr_) {
+    while (half < warps) half <<= 1;
+    half >>= 1;
   }
-  // sums over the row, the same in all of its threads (warp order)
+  // the two sums over the warp, a in lanes 0-15 and b in lanes 16-31: the
+  // first step swaps halves, so that five shuffles do
+  static __device__ __forceinline__ float warp_halves(float a, float b) {
+    const bool hi = threadIdx.x & 16;
+    float v = hi ? b : a;
+    v += __shfl_xor_sync(0xffffffffu, hi ? a : b, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  }
+  __device__ __forceinline__ void put(float v) {  // of lanes 0 and 16
+    if ((threadIdx.x & 15) == 0) red[buf][(threadIdx.x >> 4) & 1][threadIdx.x >> 5] = v;
+    asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(tpr) : "memory");
+  }
+  __device__ __forceinline__ float get(int which) const {  // 0 past the row's warps
+    const int w = threadIdx.x & 15;
+    return w < warps ? red[buf][which][warp0 + w] : 0.f;
+  }
+  // sum over the row's warps of what the 16 lanes of a half hold
+  __device__ __forceinline__ float over_warps(float v) const {
+    for (int o = half; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  }
+  // sums over the row, the same in all of its threads
   __device__ __forceinline__ float2 sum(float a, float b) {
-    float2 s = warp_sum2(a, b);
-    if (warps == 1) return s;
-    const float2* all = exchange(s);
-    s = make_float2(0.f, 0.f);
-    for (int w = 0; w < warps; ++w) {
-      s.x += all[w].x;
-      s.y += all[w].y;
+    float v = warp_halves(a, b);
+    if (warps > 1) {
+      put(v);
+      v = over_warps(get((threadIdx.x >> 4) & 1));
+      buf ^= 1;
     }
-    return s;
+    return make_float2(__shfl_sync(0xffffffffu, v, 0), __shfl_sync(0xffffffffu, v, 16));
   }
 };
 
-template <int VEC>
-__device__ __forceinline__ void norm_param(const void* p, int f32, int col, float (&v)[VEC]) {
-  if constexpr (VEC == 8) {
-    if (f32) {
-      Raw8<float> r;
-      r.load(static_cast<const float*>(p) + col);
-      r.get(v);
-    } else {
-      Raw8<__nv_bfloat16> r;
-      r.load(static_cast<const __nv_bfloat16*>(p) + col);
-      r.get(v);
-    }
-  } else {
-    v[0] = f32 ? static_cast<const float*>(p)[col]
-               : to_f32(static_cast<const __nv_bfloat16*>(p)[col]);
-  }
-}
-
 template <typename TX, int VEC>
-__device__ __forceinline__ void norm_load(const TX* p, float (&v)[VEC]) {
+__device__ __forceinline__ void norm_load(const TX* p, Lane<VEC>& v) {
   if constexpr (VEC == 8) {
     Raw8<TX> r;
     r.load(p);
     r.get(v);
   } else {
-    v[0] = to_f32(*p);
+    v.e[0] = to_f32(*p);
   }
 }
 
+template <int VEC>
+__device__ __forceinline__ void norm_param(const void* p, int f32, int64_t col, Lane<VEC>& v) {
+  if (f32) norm_load<float, VEC>(static_cast<const float*>(p) + col, v);
+  else norm_load<__nv_bfloat16, VEC>(static_cast<const __nv_bfloat16*>(p) + col, v);
+}
+
 template <typename TX, int VEC>
-__device__ __forceinline__ void norm_store(TX* p, const float (&v)[VEC]) {
+__device__ __forceinline__ void norm_store(TX* p, const Lane<VEC>& v) {
   if constexpr (VEC == 8) {
     Raw8<TX> r;
     r.set(v);
     r.store(p);
   } else {
-    *p = from_f32<TX>(v[0]);
+    *p = from_f32<TX>(v.e[0]);
   }
+}
+
+// gamma or beta in fp32 in shared memory, for kernels that pass over many rows
+// (VEC = 8): two planes of four floats a vector, so that reads do not conflict.
+__device__ __forceinline__ void norm_stage_param(const void* p, int f32, int32_t d, uint8_t* to) {
+  for (int c = threadIdx.x; c < d / 8; c += blockDim.x) {
+    Lane<8> v;
+    norm_param<8>(p, f32, 8 * c, v);
+    reinterpret_cast<ulonglong2*>(to)[c] = make_ulonglong2(v.e[0], v.e[1]);
+    reinterpret_cast<ulonglong2*>(to)[d / 8 + c] = make_ulonglong2(v.e[2], v.e[3]);
+  }
+}
+__device__ __forceinline__ void norm_staged(const uint8_t* from, int32_t d, int col, Lane<8>& v) {
+  Raw8<float> r;
+  r.load_pieces(from + 2 * col, 2 * d);
+  r.get(v);
 }
 
 // x's elements at `col` of a row, from x or from its 8 bits.
 template <typename TX, int VEC, bool Q8>
-__device__ __forceinline__ void norm_load_x(const NormBwd& p, int64_t row, int col,
-                                            float (&v)[VEC]) {
+__device__ __forceinline__ void norm_load_x(const NormBwd& p, int64_t row, int64_t col,
+                                            Lane<VEC>& v) {
   if constexpr (!Q8) {
     norm_load<TX, VEC>(static_cast<const TX*>(p.x) + row * p.d + col, v);
   } else {
@@ -179,15 +194,15 @@ __device__ __forceinline__ void norm_load_x(const NormBwd& p, int64_t row, int c
     if constexpr (VEC == 8)
       act8_unpack8(*reinterpret_cast<const uint2*>(p.q + row * p.d + col), b, v);
     else
-      v[0] = act8_value1(p.q[row * p.d + col], act8_scale(b));
+      v.e[0] = act8_value1(p.q[row * p.d + col], act8_scale(b));
   }
 }
 
 // The 8-bit copy of one vector (VEC = 8) or element: all lanes of the warp take
 // part in the groups' maxima, `on` says whether the columns exist.
 template <int VEC>
-__device__ __forceinline__ void norm_keep8(const NormFwd& p, int64_t row, int col, bool on,
-                                           const float (&v)[VEC], uint32_t top) {
+__device__ __forceinline__ void norm_keep8(const NormFwd& p, int64_t row, int64_t col, bool on,
+                                           const Lane<VEC>& v, uint32_t top) {
   if constexpr (VEC == 8) {
     uint2 qq;
     const uint32_t b = act8_pack8(v, top, qq);
@@ -196,9 +211,9 @@ __device__ __forceinline__ void norm_keep8(const NormFwd& p, int64_t row, int co
       if ((threadIdx.x & 3) == 0) p.e[row * p.groups + col / 32] = static_cast<uint8_t>(b);
     }
   } else {
-    const uint32_t b = act8_byte(__reduce_max_sync(0xffffffffu, act8_mag(v[0])));
+    const uint32_t b = act8_byte(__reduce_max_sync(0xffffffffu, act8_mag(v.e[0])));
     if (on) {
-      p.q[row * p.d + col] = static_cast<int8_t>(act8_q(v[0], act8_inv_scale(b)));
+      p.q[row * p.d + col] = static_cast<int8_t>(act8_q(v.e[0], act8_inv_scale(b)));
       if ((threadIdx.x & 31) == 0) p.e[row * p.groups + col / 32] = static_cast<uint8_t>(b);
     }
   }
@@ -210,13 +225,15 @@ __device__ __forceinline__ void norm_keep8(const NormFwd& p, int64_t row, int co
 // large mean cancels nothing), and the warps' are joined by
 //   mu = sum n_w mu_w / d,  M = sum M_w + n_w (mu_w - mu)^2.
 template <typename TX, int VEC, int NV>
-__global__ void __launch_bounds__(NORM_THREADS, NV <= 2 ? 2 : 1)
-norm_fwd_kernel(const NormFwd p) {
+__global__ void __launch_bounds__(NORM_THREADS) norm_fwd_kernel(const NormFwd p) {
   constexpr int BYTES = NORM_FWD_BYTES<TX, NV>;
   constexpr int S = norm_stages(BYTES);
+  constexpr int H = sizeof(TX) / 2;  // 16-byte pieces of a vector
+  using E = typename Lane<VEC>::E;
+  constexpr int N = Lane<VEC>::N;
   extern __shared__ __align__(16) uint8_t norm_smem[];
-  __shared__ float2 red[2][32];
-  __shared__ float cols[32];  // columns of each warp
+  __shared__ float red[2][2][16];
+  __shared__ float cols[16];  // columns of each warp
   const int t = threadIdx.x % p.tpr, group = threadIdx.x / p.tpr, G = blockDim.x / p.tpr;
   RowGroup rg(red, p.tpr);
   const float inv_d = 1.f / static_cast<float>(p.d);
@@ -228,11 +245,18 @@ norm_fwd_kernel(const NormFwd p) {
   const float nw = static_cast<float>(__reduce_add_sync(0xffffffffu, n));
   const float inv_nw = nw > 0.f ? 1.f / nw : 0.f;
   if ((threadIdx.x & 31) == 0) cols[threadIdx.x >> 5] = nw;
-  __syncthreads();
-
   // vectors of a row in shared memory: 16-byte pieces, a thread's own
-  const uint32_t ring = smem_u32(norm_smem) + threadIdx.x * 16;
   const uint32_t piece = blockDim.x * 16;
+  const uint32_t ring = smem_u32(norm_smem) + threadIdx.x * 16;
+  uint8_t* const gs = norm_smem + (VEC == 8 ? BYTES * S * blockDim.x : 0);
+  uint8_t* const bs = gs + (p.gamma ? 4 * p.d : 0);
+  if (VEC == 8 && p.staged) {
+    if (p.gamma) norm_stage_param(p.gamma, p.param_f32, p.d, gs);
+    if (p.beta) norm_stage_param(p.beta, p.param_f32, p.d, bs);
+  }
+  __syncthreads();
+  const float n_lane = (threadIdx.x & 15) < rg.warps ? cols[rg.warp0 + (threadIdx.x & 15)] : 0.f;
+
   auto fetch = [&](int64_t row, int stage) {
     if constexpr (VEC == 8) {
       if (row < p.T) {
@@ -243,8 +267,8 @@ norm_fwd_kernel(const NormFwd p) {
           const int col = (i * p.tpr + t) * VEC;
           if (col < p.d)
 #pragma unroll
-            for (int h = 0; h < static_cast<int>(sizeof(TX)) / 2; ++h)
-              cp_async16(at + (i * (sizeof(TX) / 2) + h) * piece,
+            for (int h = 0; h < H; ++h)
+              cp_async16(at + (i * H + h) * piece,
                          reinterpret_cast<const uint8_t*>(x + col) + 16 * h);
         }
       }
@@ -258,70 +282,64 @@ norm_fwd_kernel(const NormFwd p) {
   int stage = 0;
   for (; row < p.T; row += stride) {
     Raw8<TX> raw[NV];
-    float v1[NV];
+    Lane<VEC> v[NV];
     if constexpr (VEC == 8) {
-      fetch(row + (S - 1) * stride, (stage + S - 1) % S);
+      fetch(row + (S - 1) * stride, stage == 0 ? S - 1 : stage - 1);
       cp_async_wait<S - 1>();
       const uint8_t* at = norm_smem + threadIdx.x * 16 + stage * (BYTES / 16) * piece;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         raw[i].clear();
-        if ((i * p.tpr + t) * VEC < p.d) raw[i].load_pieces(at + i * (sizeof(TX) / 2) * piece, piece);
+        if ((i * p.tpr + t) * VEC < p.d) raw[i].load_pieces(at + i * H * piece, piece);
+        raw[i].get(v[i]);
       }
-      stage = (stage + 1) % S;
+      stage = stage + 1 == S ? 0 : stage + 1;
     } else {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int col = i * p.tpr + t;
-        v1[i] = col < p.d ? to_f32(static_cast<const TX*>(p.x)[row * p.d + col]) : 0.f;
+        v[i].e[0] = col < p.d ? to_f32(static_cast<const TX*>(p.x)[row * p.d + col]) : 0.f;
       }
     }
-    auto get = [&](int i, float (&v)[VEC]) {
-      if constexpr (VEC == 8) raw[i].get(v);
-      else v[0] = v1[i];
-    };
 
-    float mu = 0.f, m2 = 0.f;
+    float mu = 0.f;
     if (center) {
-      float s = 0.f;
+      E s = both<E>(0.f);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        float v[VEC];
-        get(i, v);
+      for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) s += v[j];
-      }
+        for (int j = 0; j < N; ++j) s = vadd(s, v[i].e[j]);
+      mu = vsum(s);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      mu = s * inv_nw;
+      for (int o = 16; o > 0; o >>= 1) mu += __shfl_xor_sync(0xffffffffu, mu, o);
+      mu *= inv_nw;
     }
+    E ss = both<E>(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if ((i * p.tpr + t) * VEC >= p.d) continue;
-      float v[VEC];
-      get(i, v);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) m2 = fmaf(v[j] - mu, v[j] - mu, m2);
+      for (int j = 0; j < N; ++j) {
+        const E c = vsub(v[i].e[j], both<E>(mu));
+        ss = vfma(c, c, ss);
+      }
     }
+    float m2 = vsum(ss);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
     if (rg.warps > 1) {
-      const float2* all = rg.exchange(make_float2(mu, m2));
-      const float* nws = cols + rg.warp0;
-      m2 = 0.f;
+      rg.put((threadIdx.x & 16) ? m2 : mu);
+      m2 = rg.get(1);
       if (center) {
-        mu = 0.f;
-        for (int w = 0; w < rg.warps; ++w) mu = fmaf(all[w].x, nws[w], mu);
-        mu *= inv_d;
-        for (int w = 0; w < rg.warps; ++w) {
-          const float c = all[w].x - mu;
-          m2 += fmaf(c * c, nws[w], all[w].y);
-        }
-      } else {
-        for (int w = 0; w < rg.warps; ++w) m2 += all[w].y;
+        const float muw = rg.get(0);
+        mu = rg.over_warps(muw * n_lane) * inv_d;
+        m2 = fmaf((muw - mu) * (muw - mu), n_lane, m2);
+        mu = __shfl_sync(0xffffffffu, mu, 0);
       }
+      m2 = __shfl_sync(0xffffffffu, rg.over_warps(m2), 0);
+      rg.buf ^= 1;
     }
-    const float rstd = 1.f / sqrtf(fmaf(m2, inv_d, p.eps));
+    const float rstd = rsqrtf(fmaf(m2, inv_d, p.eps));
     if (t == 0) {
       if (center) p.mean[row] = mu;
       p.rstd[row] = rstd;
@@ -330,29 +348,31 @@ norm_fwd_kernel(const NormFwd p) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int col = (i * p.tpr + t) * VEC;
-      float v[VEC];
-      get(i, v);
       if (p.q) {
         uint32_t top = 0;
         if constexpr (VEC == 8) top = raw[i].top();
-        norm_keep8<VEC>(p, row, col, col < p.d, v, top);
+        norm_keep8<VEC>(p, row, col, col < p.d, v[i], top);
       }
       if (col >= p.d) continue;
+      Lane<VEC> g, b;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) v[j] = (v[j] - mu) * rstd;
-      if (p.gamma) {
-        float g[VEC];
-        norm_param<VEC>(p.gamma, p.param_f32, col, g);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) v[j] *= g[j];
+      for (int j = 0; j < N; ++j) {
+        g.e[j] = both<E>(1.f);
+        b.e[j] = both<E>(0.f);
       }
-      if (p.beta) {
-        float b[VEC];
-        norm_param<VEC>(p.beta, p.param_f32, col, b);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) v[j] += b[j];
+      if (VEC == 8 && p.staged) {
+        if constexpr (VEC == 8) {
+          if (p.gamma) norm_staged(gs, p.d, col, g);
+          if (p.beta) norm_staged(bs, p.d, col, b);
+        }
+      } else {
+        if (p.gamma) norm_param<VEC>(p.gamma, p.param_f32, col, g);
+        if (p.beta) norm_param<VEC>(p.beta, p.param_f32, col, b);
       }
-      norm_store<TX, VEC>(static_cast<TX*>(p.y) + row * p.d + col, v);
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        b.e[j] = vfma(vmul(vsub(v[i].e[j], both<E>(mu)), both<E>(rstd)), g.e[j], b.e[j]);
+      norm_store<TX, VEC>(static_cast<TX*>(p.y) + row * p.d + col, b);
     }
   }
 }
@@ -360,30 +380,36 @@ norm_fwd_kernel(const NormFwd p) {
 // Rows of any length: a block a row, read three times.
 template <typename TX, int VEC>
 __global__ void __launch_bounds__(NORM_THREADS) norm_fwd_long_kernel(const NormFwd p) {
-  __shared__ float2 red[2][32];
+  using E = typename Lane<VEC>::E;
+  constexpr int N = Lane<VEC>::N;
+  __shared__ float red[2][2][16];
   RowGroup rg(red, NORM_THREADS);
   const float inv_d = 1.f / static_cast<float>(p.d);
   const int64_t span = static_cast<int64_t>(NORM_THREADS) * VEC;
   for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
     const TX* x = static_cast<const TX*>(p.x) + row * p.d;
-    float mu = 0.f, s = 0.f;
+    float mu = 0.f;
+    E s = both<E>(0.f);
     if (p.mean) {
       for (int64_t c = threadIdx.x * VEC; c < p.d; c += span) {
-        float v[VEC];
+        Lane<VEC> v;
         norm_load<TX, VEC>(x + c, v);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) s += v[j];
+        for (int j = 0; j < N; ++j) s = vadd(s, v.e[j]);
       }
-      mu = rg.sum(s, 0.f).x * inv_d;
-      s = 0.f;
+      mu = rg.sum(vsum(s), 0.f).x * inv_d;
+      s = both<E>(0.f);
     }
     for (int64_t c = threadIdx.x * VEC; c < p.d; c += span) {
-      float v[VEC];
+      Lane<VEC> v;
       norm_load<TX, VEC>(x + c, v);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) s = fmaf(v[j] - mu, v[j] - mu, s);
+      for (int j = 0; j < N; ++j) {
+        const E e = vsub(v.e[j], both<E>(mu));
+        s = vfma(e, e, s);
+      }
     }
-    const float rstd = 1.f / sqrtf(fmaf(rg.sum(s, 0.f).x, inv_d, p.eps));
+    const float rstd = rsqrtf(fmaf(rg.sum(vsum(s), 0.f).x, inv_d, p.eps));
     if (threadIdx.x == 0) {
       if (p.mean) p.mean[row] = mu;
       p.rstd[row] = rstd;
@@ -391,24 +417,29 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_fwd_long_kernel(const NormF
     for (int64_t c0 = 0; c0 < p.d; c0 += span) {
       const int64_t c = c0 + threadIdx.x * VEC;
       const bool on = c < p.d;
-      float v[VEC];
+      Lane<VEC> v;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) v[j] = 0.f;
-      if (on) norm_load<TX, VEC>(x + c, v);
-      if (p.q) {
-        uint32_t top = 0;
-        if constexpr (VEC == 8) top = act8_top8(v);
-        norm_keep8<VEC>(p, row, static_cast<int>(c), on, v, top);
+      for (int j = 0; j < N; ++j) v.e[j] = both<E>(0.f);
+      uint32_t top = 0;
+      if constexpr (VEC == 8) {
+        Raw8<TX> r;
+        r.clear();
+        if (on) r.load(x + c);
+        r.get(v);
+        top = r.top();
+      } else if (on) {
+        norm_load<TX, VEC>(x + c, v);
       }
+      if (p.q) norm_keep8<VEC>(p, row, c, on, v, top);
       if (!on) continue;
-      float g[VEC], b[VEC];
-      if (p.gamma) norm_param<VEC>(p.gamma, p.param_f32, static_cast<int>(c), g);
-      if (p.beta) norm_param<VEC>(p.beta, p.param_f32, static_cast<int>(c), b);
+      Lane<VEC> g, b;
+      if (p.gamma) norm_param<VEC>(p.gamma, p.param_f32, c, g);
+      if (p.beta) norm_param<VEC>(p.beta, p.param_f32, c, b);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        v[j] = (v[j] - mu) * rstd;
-        if (p.gamma) v[j] *= g[j];
-        if (p.beta) v[j] += b[j];
+      for (int j = 0; j < N; ++j) {
+        v.e[j] = vmul(vsub(v.e[j], both<E>(mu)), both<E>(rstd));
+        if (p.gamma) v.e[j] = vmul(v.e[j], g.e[j]);
+        if (p.beta) v.e[j] = vadd(v.e[j], b.e[j]);
       }
       norm_store<TX, VEC>(static_cast<TX*>(p.y) + row * p.d + c, v);
     }
@@ -421,16 +452,21 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_bwd_kernel(const NormBwd p)
   constexpr int BYTES = NORM_BWD_BYTES<TX, NV, Q8>;
   constexpr int S = norm_stages(BYTES);
   constexpr int H = sizeof(TX) / 2;  // 16-byte pieces of a vector
+  using E = typename Lane<VEC>::E;
+  constexpr int N = Lane<VEC>::N;
   extern __shared__ __align__(16) uint8_t norm_smem[];
-  __shared__ float2 red[2][32];
+  __shared__ float red[2][2][16];
   const int t = threadIdx.x % p.tpr, group = threadIdx.x / p.tpr, G = blockDim.x / p.tpr;
   RowGroup rg(red, p.tpr);
   const float inv_d = 1.f / static_cast<float>(p.d);
-  float dg[NV][VEC], db[NV][VEC];
+  Lane<VEC> dg[NV], db[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) dg[i][j] = db[i][j] = 0.f;
+    for (int j = 0; j < N; ++j) dg[i].e[j] = db[i].e[j] = both<E>(0.f);
+  uint8_t* const gs = norm_smem + (VEC == 8 ? BYTES * S * blockDim.x : 0);
+  if (VEC == 8 && p.staged && p.gamma) norm_stage_param(p.gamma, p.param_f32, p.d, gs);
+  __syncthreads();
 
   // a stage: dy's pieces, then x's, or the 8-byte pieces of q
   const uint32_t piece = blockDim.x * 16;
@@ -488,17 +524,17 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_bwd_kernel(const NormBwd p)
     ahead(row + stride);
     const uint8_t* base = norm_smem + stage * BYTES * blockDim.x;
     if constexpr (VEC == 8) {
-      fetch(row + (S - 1) * stride, (stage + S - 1) % S);
+      fetch(row + (S - 1) * stride, stage == 0 ? S - 1 : stage - 1);
       cp_async_wait<S - 1>();
-      stage = (stage + 1) % S;
+      stage = stage + 1 == S ? 0 : stage + 1;
     }
-    float a[NV][VEC], xh[NV][VEC];
-    float s1 = 0.f, s2 = 0.f;  // of a xh, of a
+    Lane<VEC> a[NV], xh[NV];
+    E s1 = both<E>(0.f), s2 = both<E>(0.f);  // of a xh, of a
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int col = (i * p.tpr + t) * VEC;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) a[i][j] = xh[i][j] = 0.f;
+      for (int j = 0; j < N; ++j) a[i].e[j] = xh[i].e[j] = both<E>(0.f);
       if (col >= p.d) continue;
       if constexpr (VEC == 8) {
         Raw8<TX> r;
@@ -516,34 +552,37 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_bwd_kernel(const NormBwd p)
         norm_load<TX, VEC>(static_cast<const TX*>(p.dy) + row * p.d + col, a[i]);
         norm_load_x<TX, VEC, Q8>(p, row, col, xh[i]);
       }
+      Lane<VEC> g;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        xh[i][j] = (xh[i][j] - mu) * rstd;
-        dg[i][j] = fmaf(a[i][j], xh[i][j], dg[i][j]);
-        db[i][j] += a[i][j];
-      }
+      for (int j = 0; j < N; ++j) g.e[j] = both<E>(1.f);
       if (p.gamma) {
-        float g[VEC];
-        norm_param<VEC>(p.gamma, p.param_f32, col, g);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) a[i][j] *= g[j];
+        if (VEC == 8 && p.staged) {
+          if constexpr (VEC == 8) norm_staged(gs, p.d, col, g);
+        } else {
+          norm_param<VEC>(p.gamma, p.param_f32, col, g);
+        }
       }
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        s1 = fmaf(a[i][j], xh[i][j], s1);
-        s2 += a[i][j];
+      for (int j = 0; j < N; ++j) {
+        const E x = vmul(vsub(xh[i].e[j], both<E>(mu)), both<E>(rstd));
+        dg[i].e[j] = vfma(a[i].e[j], x, dg[i].e[j]);
+        db[i].e[j] = vadd(db[i].e[j], a[i].e[j]);
+        a[i].e[j] = vmul(a[i].e[j], g.e[j]);
+        s1 = vfma(a[i].e[j], x, s1);
+        s2 = vadd(s2, a[i].e[j]);
+        xh[i].e[j] = x;
       }
     }
-    const float2 c = rg.sum(s1, s2);
-    const float c1 = c.x * inv_d, c2 = p.mean ? c.y * inv_d : 0.f;
+    const float2 c = rg.sum(vsum(s1), vsum(s2));
+    const E c1 = both<E>(-c.x * inv_d), c2 = both<E>(p.mean ? c.y * inv_d : 0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int col = (i * p.tpr + t) * VEC;
       if (col >= p.d) continue;
-      float dx[VEC];
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) dx[j] = rstd * (a[i][j] - c2 - xh[i][j] * c1);
-      norm_store<TX, VEC>(static_cast<TX*>(p.dx) + row * p.d + col, dx);
+      for (int j = 0; j < N; ++j)
+        a[i].e[j] = vmul(vfma(xh[i].e[j], c1, vsub(a[i].e[j], c2)), both<E>(rstd));
+      norm_store<TX, VEC>(static_cast<TX*>(p.dx) + row * p.d + col, a[i]);
     }
   }
   if (!p.want_gamma && !p.want_beta) return;
@@ -565,13 +604,13 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_bwd_kernel(const NormBwd p)
     for (int i = 0; i < NV; ++i) {
       const int col = (i * p.tpr + t) * VEC;
       if (group != 0 || col >= p.d) continue;
-      float v[VEC];
+      Lane<VEC> v;
       norm_load<float, VEC>(sums + col, v);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) dg[i][j] += v[j];
+      for (int j = 0; j < N; ++j) dg[i].e[j] = vadd(dg[i].e[j], v.e[j]);
       norm_load<float, VEC>(sums + p.d + col, v);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) db[i][j] += v[j];
+      for (int j = 0; j < N; ++j) db[i].e[j] = vadd(db[i].e[j], v.e[j]);
     }
     __syncthreads();
   }
@@ -589,41 +628,43 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_bwd_kernel(const NormBwd p)
 // Rows of any length: dx, a block a row, read twice.
 template <typename TX, int VEC, bool Q8>
 __global__ void __launch_bounds__(NORM_THREADS) norm_bwd_long_kernel(const NormBwd p) {
-  __shared__ float2 red[2][32];
+  using E = typename Lane<VEC>::E;
+  constexpr int N = Lane<VEC>::N;
+  __shared__ float red[2][2][16];
   RowGroup rg(red, NORM_THREADS);
   const float inv_d = 1.f / static_cast<float>(p.d);
   const int64_t span = static_cast<int64_t>(NORM_THREADS) * VEC;
   for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
-    const float mu = p.mean ? p.mean[row] : 0.f, rstd = p.rstd[row];
-    auto load = [&](int64_t c, float (&a)[VEC], float (&xh)[VEC]) {
+    const E mu = both<E>(p.mean ? p.mean[row] : 0.f), rstd = both<E>(p.rstd[row]);
+    auto load = [&](int64_t c, Lane<VEC>& a, Lane<VEC>& xh) {
       norm_load<TX, VEC>(static_cast<const TX*>(p.dy) + row * p.d + c, a);
-      norm_load_x<TX, VEC, Q8>(p, row, static_cast<int>(c), xh);
+      norm_load_x<TX, VEC, Q8>(p, row, c, xh);
       if (p.gamma) {
-        float g[VEC];
-        norm_param<VEC>(p.gamma, p.param_f32, static_cast<int>(c), g);
+        Lane<VEC> g;
+        norm_param<VEC>(p.gamma, p.param_f32, c, g);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) a[j] *= g[j];
+        for (int j = 0; j < N; ++j) a.e[j] = vmul(a.e[j], g.e[j]);
       }
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) xh[j] = (xh[j] - mu) * rstd;
+      for (int j = 0; j < N; ++j) xh.e[j] = vmul(vsub(xh.e[j], mu), rstd);
     };
-    float s1 = 0.f, s2 = 0.f;
+    E s1 = both<E>(0.f), s2 = both<E>(0.f);
     for (int64_t c = threadIdx.x * VEC; c < p.d; c += span) {
-      float a[VEC], xh[VEC];
+      Lane<VEC> a, xh;
       load(c, a, xh);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        s1 = fmaf(a[j], xh[j], s1);
-        s2 += a[j];
+      for (int j = 0; j < N; ++j) {
+        s1 = vfma(a.e[j], xh.e[j], s1);
+        s2 = vadd(s2, a.e[j]);
       }
     }
-    const float2 s = rg.sum(s1, s2);
-    const float c1 = s.x * inv_d, c2 = p.mean ? s.y * inv_d : 0.f;
+    const float2 s = rg.sum(vsum(s1), vsum(s2));
+    const E c1 = both<E>(-s.x * inv_d), c2 = both<E>(p.mean ? s.y * inv_d : 0.f);
     for (int64_t c = threadIdx.x * VEC; c < p.d; c += span) {
-      float a[VEC], xh[VEC];
+      Lane<VEC> a, xh;
       load(c, a, xh);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) a[j] = rstd * (a[j] - c2 - xh[j] * c1);
+      for (int j = 0; j < N; ++j) a.e[j] = vmul(vfma(xh.e[j], c1, vsub(a.e[j], c2)), rstd);
       norm_store<TX, VEC>(static_cast<TX*>(p.dx) + row * p.d + c, a);
     }
   }
@@ -638,27 +679,29 @@ __global__ void __launch_bounds__(32 * NORM_COL_WARPS) norm_cols_kernel(const No
   __shared__ float s[NORM_COL_WARPS][2 * VEC][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t col = (static_cast<int64_t>(blockIdx.x) * 32 + lane) * VEC;
-  float dg[VEC], db[VEC];
+  using E = typename Lane<VEC>::E;
+  constexpr int N = Lane<VEC>::N;
+  Lane<VEC> dg, db;
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) dg[j] = db[j] = 0.f;
+  for (int j = 0; j < N; ++j) dg.e[j] = db.e[j] = both<E>(0.f);
   if (col < p.d) {
     for (int64_t row = static_cast<int64_t>(blockIdx.y) * NORM_COL_WARPS + warp; row < p.T;
          row += static_cast<int64_t>(gridDim.y) * NORM_COL_WARPS) {
-      const float mu = p.mean ? p.mean[row] : 0.f, rstd = p.rstd[row];
-      float a[VEC], x[VEC];
+      const E mu = both<E>(p.mean ? p.mean[row] : 0.f), rstd = both<E>(p.rstd[row]);
+      Lane<VEC> a, x;
       norm_load<TX, VEC>(static_cast<const TX*>(p.dy) + row * p.d + col, a);
-      norm_load_x<TX, VEC, Q8>(p, row, static_cast<int>(col), x);
+      norm_load_x<TX, VEC, Q8>(p, row, col, x);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        dg[j] = fmaf(a[j], (x[j] - mu) * rstd, dg[j]);
-        db[j] += a[j];
+      for (int j = 0; j < N; ++j) {
+        dg.e[j] = vfma(a.e[j], vmul(vsub(x.e[j], mu), rstd), dg.e[j]);
+        db.e[j] = vadd(db.e[j], a.e[j]);
       }
     }
   }
 #pragma unroll
   for (int j = 0; j < VEC; ++j) {
-    s[warp][j][lane] = dg[j];
-    s[warp][VEC + j][lane] = db[j];
+    s[warp][j][lane] = dg.get(j);
+    s[warp][VEC + j][lane] = db.get(j);
   }
   __syncthreads();
   // thread -> (sum, column of the block)

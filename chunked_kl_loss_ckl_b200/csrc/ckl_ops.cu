@@ -85,27 +85,23 @@ struct NormShape {
   int vec, nv, tpr, threads;
 };
 
-// Two vectors a thread where a row has more than 1024 elements: half as many
-// warps to join per row.  Element-wise rows take eight elements a thread.
-// max_nv: the most vectors a thread's registers and its ring hold.
-NormShape norm_shape(int64_t d, bool vec, int max_nv) {
+// `want_nv` vectors a thread where a row has that many for two warps: what a
+// row costs a warp beside its elements (sums over lanes and warps, a barrier)
+// is then shared by more of them.  Four vectors where 512 threads need them, if
+// the kernel has that form (max_nv).
+NormShape norm_shape(int64_t d, bool vec, int want_nv, int max_nv) {
   NormShape s{vec ? 8 : 1, 0, 0, 0};
   const int64_t n = cdiv(d, s.vec);  // vectors of a row
-  const int cand_vec[] = {1, 2, 4}, cand_one[] = {8, 16};
-  const int* cand = vec ? cand_vec : cand_one;
-  const int count = vec ? 3 : 2;
-  for (int i = 0; i < count && cand[i] <= max_nv; ++i) {
-    if (vec && cand[i] == 1 && n > 128) continue;
-    if (n <= static_cast<int64_t>(ckl::NORM_THREADS) * cand[i]) {
-      s.nv = cand[i];
-      break;
-    }
-  }
-  if (s.nv == 0) return s;
+  if (n > static_cast<int64_t>(ckl::NORM_THREADS) * max_nv) return s;
+  if (!vec) s.nv = n <= ckl::NORM_THREADS * 8 ? 8 : 16;
+  else if (n > ckl::NORM_THREADS * want_nv) s.nv = 4;
+  else s.nv = n <= 32 ? 1 : n <= 64 ? 2 : want_nv;
   s.tpr = static_cast<int>(cdiv(cdiv(n, s.nv), 32) * 32);
   s.threads = ckl::NORM_THREADS / s.tpr * s.tpr;
   return s;
 }
+
+constexpr size_t kNormSmem = 220 * 1024;  // of a block, its ring and parameters
 
 template <typename P>
 int norm_launch(void (*k)(P), const P& p, dim3 grid, int threads, size_t smem, cudaStream_t st) {
@@ -127,11 +123,13 @@ int norm_fwd_launch(const ckl::NormFwd& p, const NormShape& s, int sms, cudaStre
     return norm_launch(s.vec == 8 ? ckl::norm_fwd_long_kernel<TX, 8>
                                   : ckl::norm_fwd_long_kernel<TX, 1>,
                        p, dim3(static_cast<unsigned>(rows)), ckl::NORM_THREADS, 0, st);
-  // two blocks an SM (one with four vectors a thread), every row group a row
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(p.T, sms * (s.nv == 4 ? 1 : 2))));
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(p.T, sms)));
   auto go = [&](void (*k)(ckl::NormFwd), int bytes) {
-    return norm_launch(k, p, grid, s.threads,
-                       static_cast<size_t>(s.threads) * bytes * norm_stages(bytes), st);
+    const size_t ring = static_cast<size_t>(s.threads) * bytes * norm_stages(bytes);
+    const size_t params = static_cast<size_t>(p.d) * 4 * ((p.gamma != nullptr) + (p.beta != nullptr));
+    ckl::NormFwd f = p;
+    f.staged = p.T > sms && ring + params <= kNormSmem;
+    return norm_launch(k, f, grid, s.threads, f.staged ? ring + params : ring, st);
   };
   if (s.vec == 8)
     return s.nv == 1   ? go(ckl::norm_fwd_kernel<TX, 8, 1>, NORM_FWD_BYTES<TX, 1>)
@@ -166,7 +164,10 @@ int norm_bwd_launch(const ckl::NormBwd& p, const NormShape& s, int sms, cudaStre
   const size_t sums = static_cast<size_t>(p.d) * 8;  // a row group's, on the way to the first's
   auto go = [&](void (*k)(ckl::NormBwd), int bytes) {
     const size_t ring = static_cast<size_t>(s.threads) * bytes * norm_stages(bytes);
-    return norm_launch(k, p, grid, s.threads, std::max(ring, sums), st);
+    const size_t params = p.gamma ? static_cast<size_t>(p.d) * 4 : 0;
+    ckl::NormBwd f = p;
+    f.staged = p.T > sms && ring + params <= kNormSmem;
+    return norm_launch(k, f, grid, s.threads, std::max(f.staged ? ring + params : ring, sums), st);
   };
   if (s.vec == 8) {
     if constexpr (sizeof(TX) == 2)
@@ -238,7 +239,7 @@ int ckl_norm_forward(const void* x, int32_t dtype, const void* gamma, const void
   if (T == 0) return CKL_OK;
   const bool vec = d % 8 == 0 && aligned(x, 16) && aligned(y, 16) && aligned(gamma, 16) &&
                    aligned(beta, 16) && aligned(q, 8);
-  const NormShape s = norm_shape(d, vec, vec ? 4 : 16);
+  const NormShape s = norm_shape(d, vec, 4, vec ? 4 : 16);
   ckl::NormFwd p{};
   p.x = x;
   p.gamma = gamma;
@@ -288,7 +289,7 @@ int ckl_norm_backward(const void* dy, int32_t dtype, const void* x, const int8_t
   const bool q8 = x == nullptr;
   const bool vec = d % 8 == 0 && aligned(dy, 16) && aligned(x, 16) && aligned(dx, 16) &&
                    aligned(gamma, 16) && (!q8 || aligned(q, 8));
-  const NormShape s = norm_shape(d, vec, !vec ? 16 : dtype == CKL_DTYPE_F32 ? 2 : 4);
+  const NormShape s = norm_shape(d, vec, 2, !vec ? 16 : dtype == CKL_DTYPE_F32 ? 2 : 4);
   int parts = 0;
   if (T > 0) {
     ckl::NormBwd p{};

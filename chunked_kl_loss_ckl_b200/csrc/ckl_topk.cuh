@@ -452,36 +452,6 @@ __device__ __forceinline__ uint32_t ts_gather_marked(SM& sm, const uint2* vmax,
   return sm.s_ncand;
 }
 
-// Packed pairs of fp32 (lane 0 in the low word), for the sm_100 two-lane
-// add / sub / mul instructions.
-__device__ __forceinline__ uint64_t f32x2_pack(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float f32x2_lo(uint64_t r) { return __uint_as_float(static_cast<uint32_t>(r)); }
-__device__ __forceinline__ float f32x2_hi(uint64_t r) { return __uint_as_float(static_cast<uint32_t>(r >> 32)); }
-__device__ __forceinline__ uint64_t bf16x2_widen(uint32_t w) {  // both halves, exactly
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(w << 16), "r"(w & 0xFFFF0000u));
-  return r;
-}
-__device__ __forceinline__ uint64_t f32x2_sub(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t f32x2_mul(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t f32x2_add(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 // Per-thread pass-1 state of one row: running maximum and sum of exp.
 struct TsAcc {
   float cmax = -INFINITY;  // this thread's largest value so far
