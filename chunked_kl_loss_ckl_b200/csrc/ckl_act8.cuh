@@ -88,13 +88,11 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
   return __float2bfloat16_rn(x);
 }
 
-// VEC elements of a row in registers: eight as four packed pairs of fp32 (for
-// the two-lane instructions, which halve what a row costs to issue), or one.
+// VEC elements of a row in registers: packed pairs of fp32 (for the two-lane
+// instructions, which halve what a row costs to issue), or one float.
 template <int VEC>
-struct Lane;
-template <>
-struct Lane<8> {
-  static constexpr int N = 4;
+struct Lane {
+  static constexpr int N = VEC / 2;
   using E = uint64_t;
   E e[N];
   __device__ __forceinline__ float get(int j) const {
@@ -127,20 +125,17 @@ __device__ __forceinline__ uint64_t vfma(uint64_t a, uint64_t b, uint64_t c) {
 __device__ __forceinline__ float vsum(float a) { return a; }
 __device__ __forceinline__ float vsum(uint64_t a) { return f32x2_lo(a) + f32x2_hi(a); }
 
-// Eight consecutive elements as they are in memory: one 16-byte piece of bf16
-// or two of float.
+// 16 bytes of consecutive elements as they are in memory: eight bf16 or four
+// floats.  (A float thread with eight would touch every 32-byte sector twice.)
 template <typename T>
-struct Raw8;
+constexpr int VEC16 = 16 / static_cast<int>(sizeof(T));
+template <typename T>
+struct Raw;
 template <>
-struct Raw8<__nv_bfloat16> {
+struct Raw<__nv_bfloat16> {
   uint4 a;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    a = *reinterpret_cast<const uint4*>(p);
-  }
-  // its pieces, `piece` bytes apart
-  __device__ __forceinline__ void load_pieces(const uint8_t* p, uint32_t) {
-    a = *reinterpret_cast<const uint4*>(p);
-  }
+  __device__ __forceinline__ void load(const void* p) { a = *static_cast<const uint4*>(p); }
+  __device__ __forceinline__ void store(void* p) const { *static_cast<uint4*>(p) = a; }
   __device__ __forceinline__ void clear() { a = make_uint4(0, 0, 0, 0); }
   // largest magnitude bits (as a float's), non-finite ones included
   __device__ __forceinline__ uint32_t top() const {
@@ -163,109 +158,109 @@ struct Raw8<__nv_bfloat16> {
     }
     a = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  __device__ __forceinline__ void store(__nv_bfloat16* p) const {
-    *reinterpret_cast<uint4*>(p) = a;
-  }
 };
 template <>
-struct Raw8<float> {
-  ulonglong2 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = reinterpret_cast<const ulonglong2*>(p)[0];
-    b = reinterpret_cast<const ulonglong2*>(p)[1];
-  }
-  __device__ __forceinline__ void load_pieces(const uint8_t* p, uint32_t piece) {
-    a = *reinterpret_cast<const ulonglong2*>(p);
-    b = *reinterpret_cast<const ulonglong2*>(p + piece);
-  }
-  __device__ __forceinline__ void clear() { a = b = make_ulonglong2(0ull, 0ull); }
+struct Raw<float> {
+  ulonglong2 a;
+  __device__ __forceinline__ void load(const void* p) { a = *static_cast<const ulonglong2*>(p); }
+  __device__ __forceinline__ void store(void* p) const { *static_cast<ulonglong2*>(p) = a; }
+  __device__ __forceinline__ void clear() { a = make_ulonglong2(0ull, 0ull); }
   __device__ __forceinline__ uint32_t top() const {
-    const uint64_t k = 0x7FFFFFFF7FFFFFFFull;
-    const uint64_t w[4] = {a.x & k, a.y & k, b.x & k, b.y & k};
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      m = max(m, max(static_cast<uint32_t>(w[j]), static_cast<uint32_t>(w[j] >> 32)));
-    return m;
+    const uint64_t x = a.x & 0x7FFFFFFF7FFFFFFFull, y = a.y & 0x7FFFFFFF7FFFFFFFull;
+    return max(max(static_cast<uint32_t>(x), static_cast<uint32_t>(x >> 32)),
+               max(static_cast<uint32_t>(y), static_cast<uint32_t>(y >> 32)));
   }
-  __device__ __forceinline__ void get(Lane<8>& v) const {
+  __device__ __forceinline__ void get(Lane<4>& v) const {
     v.e[0] = a.x;
     v.e[1] = a.y;
-    v.e[2] = b.x;
-    v.e[3] = b.y;
   }
-  __device__ __forceinline__ void set(const Lane<8>& v) {
-    a = make_ulonglong2(v.e[0], v.e[1]);
-    b = make_ulonglong2(v.e[2], v.e[3]);
+  __device__ __forceinline__ void set(const Lane<4>& v) { a = make_ulonglong2(v.e[0], v.e[1]); }
+};
+
+// The 8-bit form of VEC elements: VEC bytes.
+template <int VEC>
+struct Bytes {
+  uint32_t w[VEC / 4];
+  __device__ __forceinline__ void load(const void* p) {
+    if constexpr (VEC == 8) {
+      const uint2 v = *static_cast<const uint2*>(p);
+      w[0] = v.x;
+      w[1] = v.y;
+    } else {
+      w[0] = *static_cast<const uint32_t*>(p);
+    }
   }
-  __device__ __forceinline__ void store(float* p) const {
-    reinterpret_cast<ulonglong2*>(p)[0] = a;
-    reinterpret_cast<ulonglong2*>(p)[1] = b;
+  __device__ __forceinline__ void store(void* p) const {
+    if constexpr (VEC == 8) *static_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    else *static_cast<uint32_t*>(p) = w[0];
   }
 };
 
-// Eight elements of one lane to 8 bits; the four lanes of an aligned quad hold
-// one group of 32 (whole quads call it).  `top` is the lane's Raw8::top().
-// Returns the exponent byte; q is the eight bytes.  Where the group is finite
-// and both 2^(133 - b) and the sums below are normal floats, one FMA scales
-// and rounds an element: v 2^(133 - b) + 1.5 2^23 has the integer in its low
-// byte.
-__device__ __forceinline__ uint32_t act8_pack8(const Lane<8>& v, uint32_t top, uint2& q) {
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  uint32_t b = act8_byte(top);
-  uint32_t w[2];
-  if (b >= 7u && b <= 253u && top < 0x7F800000u) {
-    const float f = pow2f(133 - static_cast<int>(b));
+// VEC elements of one lane to 8 bits; 32 / VEC neighbouring lanes hold one
+// group of 32 (all of them call it).  `top` is the lane's Raw::top().  Returns
+// the exponent byte.  Where the group is finite and both 2^(133 - b) and the
+// sums below are normal floats, one FMA scales and rounds an element:
+// v 2^(133 - b) + 1.5 2^23 has the integer in its low byte.
+template <int VEC>
+__device__ __forceinline__ uint32_t act8_pack(const Lane<VEC>& v, uint32_t top, Bytes<VEC>& q) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint64_t s = f32x2_fma(v.e[2 * h], both<uint64_t>(f), both<uint64_t>(12582912.f));
-      const uint64_t t = f32x2_fma(v.e[2 * h + 1], both<uint64_t>(f), both<uint64_t>(12582912.f));
-      w[h] = __byte_perm(
+  for (int o = 1; o < 32 / VEC; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  uint32_t b = act8_byte(top);
+  if (b >= 7u && b <= 253u && top < 0x7F800000u) {
+    const uint64_t f = both<uint64_t>(pow2f(133 - static_cast<int>(b)));
+    const uint64_t c = both<uint64_t>(12582912.f);
+#pragma unroll
+    for (int h = 0; h < VEC / 4; ++h) {
+      const uint64_t s = f32x2_fma(v.e[2 * h], f, c), t = f32x2_fma(v.e[2 * h + 1], f, c);
+      q.w[h] = __byte_perm(
           __byte_perm(static_cast<uint32_t>(s), static_cast<uint32_t>(s >> 32), 0x0040),
           __byte_perm(static_cast<uint32_t>(t), static_cast<uint32_t>(t >> 32), 0x0040), 0x5410);
     }
-  } else {  // the same for the whole quad
-    const uint32_t quad = 0xFu << (threadIdx.x & 28u);
+  } else {  // the same in all of the group's lanes
+    constexpr uint32_t LANES = 32 / VEC;
+    const uint32_t mask = ((1u << LANES) - 1u) << (threadIdx.x & (32u - LANES));
     uint32_t a = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) a = max(a, act8_mag(v.get(j)));
-    a = max(a, __shfl_xor_sync(quad, a, 1));
-    a = max(a, __shfl_xor_sync(quad, a, 2));
+    for (int j = 0; j < VEC; ++j) a = max(a, act8_mag(v.get(j)));
+#pragma unroll
+    for (int o = 1; o < static_cast<int>(LANES); o <<= 1) a = max(a, __shfl_xor_sync(mask, a, o));
     b = act8_byte(a);
     const Act8Scale s = act8_inv_scale(b);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      w[h] = act8_q(v.get(4 * h), s) | (act8_q(v.get(4 * h + 1), s) << 8) |
-             (act8_q(v.get(4 * h + 2), s) << 16) | (act8_q(v.get(4 * h + 3), s) << 24);
+    for (int h = 0; h < VEC / 4; ++h)
+      q.w[h] = act8_q(v.get(4 * h), s) | (act8_q(v.get(4 * h + 1), s) << 8) |
+               (act8_q(v.get(4 * h + 2), s) << 16) | (act8_q(v.get(4 * h + 3), s) << 24);
   }
-  q = make_uint2(w[0], w[1]);
   return b;
 }
 
-// The values of eight bytes.  Where 2^(b - 133) and 2^23 times it are normal
+// The values of VEC bytes.  Where 2^(b - 133) and 2^23 times it are normal
 // floats and no byte is -128, one FMA an element: (2^23 + 128 + q) s - (2^23 +
 // 128) s, both products exact.
-__device__ __forceinline__ void act8_unpack8(uint2 q, uint32_t b, Lane<8>& v) {
-  const uint32_t x = q.x ^ 0x80808080u, y = q.y ^ 0x80808080u;  // q + 128: 0 marks a NaN
-  const uint32_t nan = ((x - 0x01010101u) & ~x) | ((y - 0x01010101u) & ~y);
+template <int VEC>
+__device__ __forceinline__ void act8_unpack(const Bytes<VEC>& q, uint32_t b, Lane<VEC>& v) {
+  uint32_t x[VEC / 4], nan = 0;
+#pragma unroll
+  for (int h = 0; h < VEC / 4; ++h) {
+    x[h] = q.w[h] ^ 0x80808080u;  // q + 128: 0 marks a NaN
+    nan |= (x[h] - 0x01010101u) & ~x[h];
+  }
   if (b >= 7u && b <= 228u && (nan & 0x80808080u) == 0u) {
     const float s = pow2f(static_cast<int>(b) - 133);
     const uint64_t s2 = both<uint64_t>(s), c2 = both<uint64_t>(-8388736.f * s);
     const uint32_t k = 0x4B000000u;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t w = h ? y : x;
-      v.e[2 * h] = f32x2_fma(f32x2_pack(__uint_as_float(__byte_perm(w, k, 0x7440)),
-                                        __uint_as_float(__byte_perm(w, k, 0x7441))), s2, c2);
-      v.e[2 * h + 1] = f32x2_fma(f32x2_pack(__uint_as_float(__byte_perm(w, k, 0x7442)),
-                                            __uint_as_float(__byte_perm(w, k, 0x7443))), s2, c2);
+    for (int h = 0; h < VEC / 4; ++h) {
+      v.e[2 * h] = f32x2_fma(f32x2_pack(__uint_as_float(__byte_perm(x[h], k, 0x7440)),
+                                        __uint_as_float(__byte_perm(x[h], k, 0x7441))), s2, c2);
+      v.e[2 * h + 1] = f32x2_fma(f32x2_pack(__uint_as_float(__byte_perm(x[h], k, 0x7442)),
+                                            __uint_as_float(__byte_perm(x[h], k, 0x7443))), s2, c2);
     }
   } else {
     const Act8Scale s = act8_scale(b);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t w = (j < 2 ? q.x : q.y) >> (16 * (j & 1));
+    for (int j = 0; j < VEC / 2; ++j) {
+      const uint32_t w = q.w[j / 2] >> (16 * (j & 1));
       v.e[j] = f32x2_pack(act8_value1(static_cast<int8_t>(w & 0xFFu), s),
                           act8_value1(static_cast<int8_t>((w >> 8) & 0xFFu), s));
     }
@@ -273,9 +268,9 @@ __device__ __forceinline__ void act8_unpack8(uint2 q, uint32_t b, Lane<8>& v) {
 }
 
 // ------------------------------------------------------------------- kernels
-// Rows of T x d elements, `units` units of a group (VEC: four lanes with eight
-// elements each, d % 8 == 0 and 16-byte rows; otherwise a warp, an element a
-// lane) taken in a grid-stride loop.  A thread's next unit is found from its
+// Rows of T x d elements, `units` units of a group (32 / VEC lanes with VEC
+// elements each: 16 bytes where rows allow it, or an element a lane) taken in a
+// grid-stride loop.  A thread's next unit is found from its
 // last one by adding the stride's rows and groups, so that only the first
 // costs a division.
 struct Act8Pos {
@@ -298,11 +293,12 @@ struct Act8Pos {
 
 constexpr int ACT8_UNROLL = 4;  // vectors a thread loads before it works on them
 
-template <typename TX, bool VEC>
+template <typename TX, int VEC>
 __global__ void __launch_bounds__(ACT8_THREADS)
 act8_pack_kernel(const TX* __restrict__ x, int64_t T, int32_t d, int32_t groups,
                  int8_t* __restrict__ q, uint8_t* __restrict__ e) {
-  constexpr int LANES = VEC ? 4 : 32;  // lanes of a unit
+  constexpr int LANES = 32 / VEC;  // lanes of a unit
+  using R = typename std::conditional<VEC == 1, float, Raw<TX>>::type;
   const int sub = threadIdx.x % LANES;
   const int64_t tid = static_cast<int64_t>(blockIdx.x) * ACT8_THREADS + threadIdx.x;
   const int64_t nthr = static_cast<int64_t>(gridDim.x) * ACT8_THREADS;
@@ -311,70 +307,63 @@ act8_pack_kernel(const TX* __restrict__ x, int64_t T, int32_t d, int32_t groups,
   // whole warps take part in the group maxima: the loop runs while the
   // warp's first lane has a unit
   for (int64_t u = (tid & ~int64_t(31)) / LANES; u < units; u += ACT8_UNROLL * step) {
-    Act8Pos at[ACT8_UNROLL] = {p, p, p, p};
-    if constexpr (VEC) {
-      Raw8<TX> r[ACT8_UNROLL];
+    R r[ACT8_UNROLL];
+    int64_t at[ACT8_UNROLL], at_e[ACT8_UNROLL];  // first element (-1: none), exponent
 #pragma unroll
-      for (int k = 0; k < ACT8_UNROLL; ++k) {
-        at[k] = p;
-        p.next(groups);
+    for (int k = 0; k < ACT8_UNROLL; ++k) {
+      const int32_t c = p.g * 32 + sub * VEC;
+      at[k] = p.row < T && c < d ? p.row * d + c : -1;
+      at_e[k] = p.row * groups + p.g;
+      if constexpr (VEC == 1) {
+        r[k] = at[k] >= 0 ? to_f32(x[at[k]]) : 0.f;
+      } else {
         r[k].clear();
-        if (at[k].row < T && at[k].g * 32 + sub * 8 < d)
-          r[k].load(x + at[k].row * d + at[k].g * 32 + sub * 8);
+        if (at[k] >= 0) r[k].load(x + at[k]);
       }
+      p.next(groups);
+    }
 #pragma unroll
-      for (int k = 0; k < ACT8_UNROLL; ++k) {
-        Lane<8> v;
+    for (int k = 0; k < ACT8_UNROLL; ++k) {
+      if constexpr (VEC == 1) {
+        const uint32_t b = act8_byte(__reduce_max_sync(0xffffffffu, act8_mag(r[k])));
+        if (at[k] < 0) continue;
+        q[at[k]] = static_cast<int8_t>(act8_q(r[k], act8_inv_scale(b)));
+        if (sub == 0) e[at_e[k]] = static_cast<uint8_t>(b);
+      } else {
+        Lane<VEC> v;
         r[k].get(v);
-        uint2 qq;
-        const uint32_t b = act8_pack8(v, r[k].top(), qq);
-        if (at[k].row < T && at[k].g * 32 + sub * 8 < d) {
-          *reinterpret_cast<uint2*>(q + at[k].row * d + at[k].g * 32 + sub * 8) = qq;
-          if (sub == 0) e[at[k].row * groups + at[k].g] = static_cast<uint8_t>(b);
-        }
-      }
-    } else {
-      float v[ACT8_UNROLL];
-#pragma unroll
-      for (int k = 0; k < ACT8_UNROLL; ++k) {
-        at[k] = p;
-        p.next(groups);
-        const int32_t c = at[k].g * 32 + sub;
-        v[k] = at[k].row < T && c < d ? to_f32(x[at[k].row * d + c]) : 0.f;
-      }
-#pragma unroll
-      for (int k = 0; k < ACT8_UNROLL; ++k) {
-        const int32_t c = at[k].g * 32 + sub;
-        const uint32_t b = act8_byte(__reduce_max_sync(0xffffffffu, act8_mag(v[k])));
-        if (at[k].row >= T) continue;
-        if (c < d) q[at[k].row * d + c] = static_cast<int8_t>(act8_q(v[k], act8_inv_scale(b)));
-        if (sub == 0) e[at[k].row * groups + at[k].g] = static_cast<uint8_t>(b);
+        Bytes<VEC> bytes;
+        const uint32_t b = act8_pack<VEC>(v, r[k].top(), bytes);
+        if (at[k] < 0) continue;
+        bytes.store(q + at[k]);
+        if (sub == 0) e[at_e[k]] = static_cast<uint8_t>(b);
       }
     }
   }
 }
 
-template <typename TX, bool VEC>
+template <typename TX, int VEC>
 __global__ void __launch_bounds__(ACT8_THREADS)
 act8_unpack_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ e, int64_t T,
                    int32_t d, int32_t groups, TX* __restrict__ x) {
-  constexpr int LANES = VEC ? 4 : 32;
-  using Q = typename std::conditional<VEC, uint2, int8_t>::type;
+  constexpr int LANES = 32 / VEC;
+  using Q = typename std::conditional<VEC == 1, int8_t, Bytes<VEC == 1 ? 4 : VEC>>::type;
   const int sub = threadIdx.x % LANES;
   const int64_t tid = static_cast<int64_t>(blockIdx.x) * ACT8_THREADS + threadIdx.x;
   const int64_t nthr = static_cast<int64_t>(gridDim.x) * ACT8_THREADS;
   const int64_t units = T * groups, step = nthr / LANES;
   Act8Pos p(tid / LANES, step, groups);
   for (int64_t u = tid / LANES; u < units; u += ACT8_UNROLL * step) {
-    Q qq[ACT8_UNROLL];
+    Q bytes[ACT8_UNROLL];
     uint32_t b[ACT8_UNROLL];
     int64_t at[ACT8_UNROLL];  // first element, -1: none
 #pragma unroll
     for (int k = 0; k < ACT8_UNROLL; ++k) {
-      const int32_t c = p.g * 32 + sub * (VEC ? 8 : 1);
+      const int32_t c = p.g * 32 + sub * VEC;
       at[k] = p.row < T && c < d ? p.row * d + c : -1;
       if (at[k] >= 0) {
-        qq[k] = *reinterpret_cast<const Q*>(q + at[k]);
+        if constexpr (VEC == 1) bytes[k] = q[at[k]];
+        else bytes[k].load(q + at[k]);
         b[k] = e[p.row * groups + p.g];
       }
       p.next(groups);
@@ -382,14 +371,14 @@ act8_unpack_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ e, 
 #pragma unroll
     for (int k = 0; k < ACT8_UNROLL; ++k) {
       if (at[k] < 0) continue;
-      if constexpr (VEC) {
-        Lane<8> v;
-        act8_unpack8(qq[k], b[k], v);
-        Raw8<TX> r;
+      if constexpr (VEC == 1) {
+        x[at[k]] = from_f32<TX>(act8_value1(bytes[k], act8_scale(b[k])));
+      } else {
+        Lane<VEC> v;
+        act8_unpack<VEC>(bytes[k], b[k], v);
+        Raw<TX> r;
         r.set(v);
         r.store(x + at[k]);
-      } else {
-        x[at[k]] = from_f32<TX>(act8_value1(qq[k], act8_scale(b[k])));
       }
     }
   }

@@ -10,12 +10,12 @@
 // registers.  A row belongs to a group of `tpr` threads (whole warps); a
 // thread holds NV vectors of VEC elements, vector i at column (i tpr + t) VEC,
 // so loads are coalesced and a thread's columns are the same in every row.
-// VEC = 8 (16-byte loads) needs d % 8 == 0 and 16-byte pointers; VEC = 1 takes
-// the rest.  Groups take rows in a grid-stride loop.
+// 16-byte loads (VEC = 8 bf16, 4 fp32) need d % VEC == 0 and 16-byte pointers;
+// VEC = 1 takes the rest.  Groups take rows in a grid-stride loop.
 //
 // An SM needs about 35 KB of loads under way to keep HBM busy, and a row's
 // sums are a dependent chain during which a thread would load nothing.  So
-// with VEC = 8 a thread copies its own vectors of the next rows to shared
+// with 16-byte loads a thread copies its own vectors of the next rows to shared
 // memory (cp.async, NORM stages of them) and only ever reads what it copied
 // itself: no barrier and no wait on another thread.
 //
@@ -36,6 +36,7 @@
 namespace ckl {
 
 constexpr int NORM_THREADS = 512;
+constexpr int NORM_WARPS = 32;  // of a block, at most
 constexpr int NORM_MAX_PARTS = 592;  // blocks whose gradient sums the workspace holds
 
 struct NormFwd {
@@ -48,7 +49,7 @@ struct NormFwd {
   int8_t* q;  // null: no 8-bit copy of x
   uint8_t* e;
   int64_t T;
-  int32_t d, groups, tpr, param_f32, staged;  // staged: the parameters go to shared memory
+  int32_t d, groups, tpr, param_f32;
   float eps;
 };
 
@@ -63,14 +64,19 @@ struct NormBwd {
   void* dx;
   float* parts;  // [parts, 2, d]: sums of dgamma and dbeta
   int64_t T;
-  int32_t d, groups, tpr, param_f32, staged, want_gamma, want_beta;
+  int32_t d, groups, tpr, param_f32, want_gamma, want_beta;
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// n = 16 (4, 8) bytes, or 0: zeros are written and nothing is read.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
 }
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+template <int BYTES>
+__device__ __forceinline__ void cp_async_bytes(uint32_t dst, const void* src, uint32_t n) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES),
+               "r"(n)
+               : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -80,60 +86,67 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Stages of a ring whose stage takes `bytes` a thread: four where 512 threads'
-// fit in 200 KB, otherwise as many as do.
-__host__ __device__ constexpr int norm_stages(int bytes) {
-  return 200 * 1024 / (NORM_THREADS * bytes) >= 4 ? 4 : 200 * 1024 / (NORM_THREADS * bytes);
+// Stages of a ring whose stage takes `bytes` a thread: as many as fit in 200 KB
+// for the block's threads, four at most.
+__host__ __device__ constexpr int norm_stages(int bytes, int threads) {
+  return 200 * 1024 / (threads * bytes) >= 4 ? 4 : 200 * 1024 / (threads * bytes);
 }
-template <typename TX, int NV>
-constexpr int NORM_FWD_BYTES = NV * 8 * static_cast<int>(sizeof(TX));
+// Of the forward where two blocks share an SM.
+__host__ __device__ constexpr int norm_fwd_stages(int bytes) { return bytes <= 32 ? 3 : 2; }
+template <int NV>
+constexpr int NORM_FWD_BYTES = NV * 16;
 template <typename TX, int NV, bool Q8>
-constexpr int NORM_BWD_BYTES = NV * 8 * (static_cast<int>(sizeof(TX)) * (Q8 ? 1 : 2) + (Q8 ? 1 : 0));
+constexpr int NORM_BWD_BYTES = NV * (16 + (Q8 ? VEC16<TX> : 16));
 
-// What the warps of a row's group tell each other through shared memory.  Two
-// buffers take turns, so that one barrier an exchange is enough.  Warp w's two
-// numbers are at [0][w] and [1][w]; lanes 0-15 and 16-31 read one of the two
-// each and add them up in a butterfly, so that the sums cost the same few
-// instructions however many warps a row has.
+// What the warps of a row's group tell each other through shared memory: two
+// numbers a warp.  Two buffers take turns, so that one barrier an exchange is
+// enough.  Lane l reads those of warp l mod `span` (4, 8 or 16, at least the
+// row's warps; of two warps where a row has more than 16), so that log2(span)
+// butterfly steps leave a sum over the warps in every lane of a half.
 struct RowGroup {
-  float (*red)[2][16];
-  int buf, warp0, warps, half, bar, tpr;
-  __device__ __forceinline__ RowGroup(float (*r)[2][16], int tpr_)
-      : red(r), buf(0), warp0((threadIdx.x / tpr_) * (tpr_ / 32)), warps(tpr_ / 32), half(1),
-        bar(1 + threadIdx.x / tpr_), tpr(tpr_) {
-    while (half < warps) half <<= 1;
-    half >>= 1;
+  float2* red;  // [2][NORM_WARPS]
+  int buf, warps, span, at, bar, tpr;
+  bool on;  // the lane's warp exists
+  __device__ __forceinline__ RowGroup(float2* r, int tpr_)
+      : red(r), buf(0), warps(tpr_ / 32), bar(1 + threadIdx.x / tpr_), tpr(tpr_) {
+    span = warps <= 4 ? 4 : warps <= 8 ? 8 : 16;
+    const int w = threadIdx.x & (span - 1);
+    on = w < warps;
+    at = (threadIdx.x / tpr_) * warps + (on ? w : 0);
   }
-  // the two sums over the warp, a in lanes 0-15 and b in lanes 16-31: the
-  // first step swaps halves, so that five shuffles do
-  static __device__ __forceinline__ float warp_halves(float a, float b) {
+  __device__ __forceinline__ void barrier() const {
+    asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(tpr) : "memory");
+  }
+  __device__ __forceinline__ float2 exchange(float a, float b) {
+    if ((threadIdx.x & 31) == 0) red[buf + (threadIdx.x >> 5)] = make_float2(a, b);
+    barrier();
+    const float2 v = red[buf + at];
+    buf ^= NORM_WARPS;
+    return v;
+  }
+  __device__ __forceinline__ float over_warps(float v) const {
+    if (span > 8) v += __shfl_xor_sync(0xffffffffu, v, 8);
+    if (span > 4) v += __shfl_xor_sync(0xffffffffu, v, 4);
+    v += __shfl_xor_sync(0xffffffffu, v, 2);
+    return v + __shfl_xor_sync(0xffffffffu, v, 1);
+  }
+  // Sums over the row, the same in all of its threads.  The first step swaps
+  // halves: lanes 0-15 go on with a, 16-31 with b, so that two sums take the
+  // shuffles of one.
+  __device__ __forceinline__ float2 sum(float a, float b) {
     const bool hi = threadIdx.x & 16;
     float v = hi ? b : a;
     v += __shfl_xor_sync(0xffffffffu, hi ? a : b, 16);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-  }
-  __device__ __forceinline__ void put(float v) {  // of lanes 0 and 16
-    if ((threadIdx.x & 15) == 0) red[buf][(threadIdx.x >> 4) & 1][threadIdx.x >> 5] = v;
-    asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(tpr) : "memory");
-  }
-  __device__ __forceinline__ float get(int which) const {  // 0 past the row's warps
-    const int w = threadIdx.x & 15;
-    return w < warps ? red[buf][which][warp0 + w] : 0.f;
-  }
-  // sum over the row's warps of what the 16 lanes of a half hold
-  __device__ __forceinline__ float over_warps(float v) const {
-    for (int o = half; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-  }
-  // sums over the row, the same in all of its threads
-  __device__ __forceinline__ float2 sum(float a, float b) {
-    float v = warp_halves(a, b);
     if (warps > 1) {
-      put(v);
-      v = over_warps(get((threadIdx.x >> 4) & 1));
-      buf ^= 1;
+      float* f = reinterpret_cast<float*>(red + buf);
+      if ((threadIdx.x & 15) == 0) f[2 * (threadIdx.x >> 5) + hi] = v;
+      barrier();
+      v = on ? f[2 * at + hi] : 0.f;
+      if (warps > 16 && (threadIdx.x & 15) + 16 < warps) v += f[2 * (at + 16) + hi];
+      v = over_warps(v);
+      buf ^= NORM_WARPS;
     }
     return make_float2(__shfl_sync(0xffffffffu, v, 0), __shfl_sync(0xffffffffu, v, 16));
   }
@@ -141,46 +154,84 @@ struct RowGroup {
 
 template <typename TX, int VEC>
 __device__ __forceinline__ void norm_load(const TX* p, Lane<VEC>& v) {
-  if constexpr (VEC == 8) {
-    Raw8<TX> r;
+  if constexpr (VEC == 1) {
+    v.e[0] = to_f32(*p);
+  } else if constexpr (VEC == VEC16<TX>) {
+    Raw<TX> r;
     r.load(p);
     r.get(v);
-  } else {
-    v.e[0] = to_f32(*p);
+  } else if constexpr (sizeof(TX) == 4) {  // eight floats
+    Raw<float> r;
+    Lane<4> lo, hi;
+    r.load(p);
+    r.get(lo);
+    r.load(p + 4);
+    r.get(hi);
+    v.e[0] = lo.e[0];
+    v.e[1] = lo.e[1];
+    v.e[2] = hi.e[0];
+    v.e[3] = hi.e[1];
+  } else {  // four bf16
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
+    v.e[0] = bf16x2_widen(w.x);
+    v.e[1] = bf16x2_widen(w.y);
   }
 }
 
+// gamma's or beta's elements, `none` each without one.
 template <int VEC>
-__device__ __forceinline__ void norm_param(const void* p, int f32, int64_t col, Lane<VEC>& v) {
-  if (f32) norm_load<float, VEC>(static_cast<const float*>(p) + col, v);
-  else norm_load<__nv_bfloat16, VEC>(static_cast<const __nv_bfloat16*>(p) + col, v);
+__device__ __forceinline__ void norm_param(const void* p, int f32, float none, int64_t col,
+                                           Lane<VEC>& v) {
+  if (p == nullptr) {
+#pragma unroll
+    for (int j = 0; j < Lane<VEC>::N; ++j) v.e[j] = both<typename Lane<VEC>::E>(none);
+  } else if (f32) {
+    norm_load<float, VEC>(static_cast<const float*>(p) + col, v);
+  } else {
+    norm_load<__nv_bfloat16, VEC>(static_cast<const __nv_bfloat16*>(p) + col, v);
+  }
 }
 
 template <typename TX, int VEC>
 __device__ __forceinline__ void norm_store(TX* p, const Lane<VEC>& v) {
-  if constexpr (VEC == 8) {
-    Raw8<TX> r;
+  if constexpr (VEC == 1) {
+    *p = from_f32<TX>(v.e[0]);
+  } else if constexpr (VEC == VEC16<TX>) {
+    Raw<TX> r;
     r.set(v);
     r.store(p);
-  } else {
-    *p = from_f32<TX>(v.e[0]);
+  } else {  // eight floats (sums of the gradients)
+    static_assert(sizeof(TX) == 4 && VEC == 8, "sums are floats");
+    reinterpret_cast<ulonglong2*>(p)[0] = make_ulonglong2(v.e[0], v.e[1]);
+    reinterpret_cast<ulonglong2*>(p)[1] = make_ulonglong2(v.e[2], v.e[3]);
   }
 }
 
-// gamma or beta in fp32 in shared memory, for kernels that pass over many rows
-// (VEC = 8): two planes of four floats a vector, so that reads do not conflict.
-__device__ __forceinline__ void norm_stage_param(const void* p, int f32, int32_t d, uint8_t* to) {
-  for (int c = threadIdx.x; c < d / 8; c += blockDim.x) {
-    Lane<8> v;
-    norm_param<8>(p, f32, 8 * c, v);
-    reinterpret_cast<ulonglong2*>(to)[c] = make_ulonglong2(v.e[0], v.e[1]);
-    reinterpret_cast<ulonglong2*>(to)[d / 8 + c] = make_ulonglong2(v.e[2], v.e[3]);
+// gamma or beta in fp32 in shared memory, for kernels that pass over many rows:
+// planes of four floats a vector, so that reads do not conflict, filled up to
+// the threads' columns (span >= d).
+template <int VEC>
+__device__ __forceinline__ void norm_stage_param(const void* p, int f32, float none, int32_t d,
+                                                 int32_t span, uint8_t* to) {
+  for (int c = threadIdx.x; c < span / VEC; c += blockDim.x) {
+    Lane<VEC> v;
+    norm_param<VEC>(VEC * c < d ? p : nullptr, f32, none, VEC * c, v);
+#pragma unroll
+    for (int h = 0; h < VEC / 4; ++h)
+      reinterpret_cast<ulonglong2*>(to)[h * (span / VEC) + c] =
+          make_ulonglong2(v.e[2 * h], v.e[2 * h + 1]);
   }
 }
-__device__ __forceinline__ void norm_staged(const uint8_t* from, int32_t d, int col, Lane<8>& v) {
-  Raw8<float> r;
-  r.load_pieces(from + 2 * col, 2 * d);
-  r.get(v);
+template <int VEC>
+__device__ __forceinline__ void norm_staged(const uint8_t* from, int32_t span, int col,
+                                            Lane<VEC>& v) {
+#pragma unroll
+  for (int h = 0; h < VEC / 4; ++h) {
+    const ulonglong2 w =
+        reinterpret_cast<const ulonglong2*>(from)[h * (span / VEC) + col / VEC];
+    v.e[2 * h] = w.x;
+    v.e[2 * h + 1] = w.y;
+  }
 }
 
 // x's elements at `col` of a row, from x or from its 8 bits.
@@ -191,24 +242,27 @@ __device__ __forceinline__ void norm_load_x(const NormBwd& p, int64_t row, int64
     norm_load<TX, VEC>(static_cast<const TX*>(p.x) + row * p.d + col, v);
   } else {
     const uint32_t b = p.e[row * p.groups + col / 32];
-    if constexpr (VEC == 8)
-      act8_unpack8(*reinterpret_cast<const uint2*>(p.q + row * p.d + col), b, v);
-    else
+    if constexpr (VEC == 1) {
       v.e[0] = act8_value1(p.q[row * p.d + col], act8_scale(b));
+    } else {
+      Bytes<VEC> q;
+      q.load(p.q + row * p.d + col);
+      act8_unpack<VEC>(q, b, v);
+    }
   }
 }
 
-// The 8-bit copy of one vector (VEC = 8) or element: all lanes of the warp take
+// The 8-bit copy of one vector or element: all lanes of the warp take
 // part in the groups' maxima, `on` says whether the columns exist.
 template <int VEC>
 __device__ __forceinline__ void norm_keep8(const NormFwd& p, int64_t row, int64_t col, bool on,
                                            const Lane<VEC>& v, uint32_t top) {
-  if constexpr (VEC == 8) {
-    uint2 qq;
-    const uint32_t b = act8_pack8(v, top, qq);
+  if constexpr (VEC > 1) {
+    Bytes<VEC> q;
+    const uint32_t b = act8_pack<VEC>(v, top, q);
     if (on) {
-      *reinterpret_cast<uint2*>(p.q + row * p.d + col) = qq;
-      if ((threadIdx.x & 3) == 0) p.e[row * p.groups + col / 32] = static_cast<uint8_t>(b);
+      q.store(p.q + row * p.d + col);
+      if (threadIdx.x % (32 / VEC) == 0) p.e[row * p.groups + col / 32] = static_cast<uint8_t>(b);
     }
   } else {
     const uint32_t b = act8_byte(__reduce_max_sync(0xffffffffu, act8_mag(v.e[0])));
@@ -224,82 +278,109 @@ __device__ __forceinline__ void norm_keep8(const NormFwd& p, int64_t row, int64_
 // takes both of its own columns (the squares about the warp's mean, so that a
 // large mean cancels nothing), and the warps' are joined by
 //   mu = sum n_w mu_w / d,  M = sum M_w + n_w (mu_w - mu)^2.
-template <typename TX, int VEC, int NV>
-__global__ void __launch_bounds__(NORM_THREADS) norm_fwd_kernel(const NormFwd p) {
-  constexpr int BYTES = NORM_FWD_BYTES<TX, NV>;
-  constexpr int S = norm_stages(BYTES);
-  constexpr int H = sizeof(TX) / 2;  // 16-byte pieces of a vector
+//
+// STAGED: gamma and beta in shared memory and 64 registers, so that two blocks
+// run on an SM (the sums are a chain of shuffles that only other warps hide);
+// otherwise they are in registers.  KEEP: x's 8 bits are written too.
+template <typename TX, int VEC, int NV, bool STAGED, bool KEEP>
+__global__ void __launch_bounds__(NORM_THREADS, STAGED ? 2 : 1) norm_fwd_kernel(const NormFwd p) {
+  constexpr int BYTES = NORM_FWD_BYTES<NV>;
+  constexpr int S =
+      VEC == 1 ? 1 : STAGED ? norm_fwd_stages(BYTES) : norm_stages(BYTES, NORM_THREADS);
   using E = typename Lane<VEC>::E;
   constexpr int N = Lane<VEC>::N;
   extern __shared__ __align__(16) uint8_t norm_smem[];
-  __shared__ float red[2][2][16];
-  __shared__ float cols[16];  // columns of each warp
+  __shared__ float2 red[2 * NORM_WARPS];
+  __shared__ float cols[NORM_WARPS];  // columns of each warp
   const int t = threadIdx.x % p.tpr, group = threadIdx.x / p.tpr, G = blockDim.x / p.tpr;
   RowGroup rg(red, p.tpr);
   const float inv_d = 1.f / static_cast<float>(p.d);
   const bool center = p.mean != nullptr;
+  const int step = p.tpr * VEC;  // columns from a thread's vector to its next
+  const int col0 = t * VEC;
+  // only a thread's last vector may be past the row's end: it is zeros then,
+  // worked on like the others and not stored
+  auto on = [&](int i) { return (VEC > 1 && i < NV - 1) || col0 + i * step < p.d; };
+  const float last = on(NV - 1) ? 1.f : 0.f;
   int n = 0;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
-    if ((i * p.tpr + t) * VEC < p.d) n += VEC;
+    if (on(i)) n += VEC;
   const float nw = static_cast<float>(__reduce_add_sync(0xffffffffu, n));
   const float inv_nw = nw > 0.f ? 1.f / nw : 0.f;
   if ((threadIdx.x & 31) == 0) cols[threadIdx.x >> 5] = nw;
   // vectors of a row in shared memory: 16-byte pieces, a thread's own
-  const uint32_t piece = blockDim.x * 16;
-  const uint32_t ring = smem_u32(norm_smem) + threadIdx.x * 16;
-  uint8_t* const gs = norm_smem + (VEC == 8 ? BYTES * S * blockDim.x : 0);
-  uint8_t* const bs = gs + (p.gamma ? 4 * p.d : 0);
-  if (VEC == 8 && p.staged) {
-    if (p.gamma) norm_stage_param(p.gamma, p.param_f32, p.d, gs);
-    if (p.beta) norm_stage_param(p.beta, p.param_f32, p.d, bs);
-  }
-  __syncthreads();
-  const float n_lane = (threadIdx.x & 15) < rg.warps ? cols[rg.warp0 + (threadIdx.x & 15)] : 0.f;
+  const uint32_t piece = blockDim.x * 16, stage_bytes = BYTES * blockDim.x;
+  uint8_t* const mine = norm_smem + threadIdx.x * 16;
 
-  auto fetch = [&](int64_t row, int stage) {
-    if constexpr (VEC == 8) {
-      if (row < p.T) {
-        const TX* x = static_cast<const TX*>(p.x) + row * p.d;
-        const uint32_t at = ring + stage * (BYTES / 16) * piece;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * G;
+  int64_t row = static_cast<int64_t>(gridDim.x) * group + blockIdx.x;
+  int64_t row_in = row;  // the next row to fetch
+  const TX* in = static_cast<const TX*>(p.x) + row * p.d + col0;
+  auto fetch = [&](uint32_t at) {
+    if constexpr (VEC > 1) {
+      if (row_in < p.T) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int col = (i * p.tpr + t) * VEC;
-          if (col < p.d)
-#pragma unroll
-            for (int h = 0; h < H; ++h)
-              cp_async16(at + (i * H + h) * piece,
-                         reinterpret_cast<const uint8_t*>(x + col) + 16 * h);
-        }
+        for (int i = 0; i < NV; ++i)
+          cp_async16(at + i * piece, in + (on(i) ? i * step : 0), on(i) ? 16u : 0u);
+        row_in += stride;
+        in += stride * p.d;
       }
       cp_async_commit();
     }
   };
-
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * G;
-  int64_t row = static_cast<int64_t>(gridDim.x) * group + blockIdx.x;
-  for (int s = 0; s < S - 1; ++s) fetch(row + s * stride, s);
-  int stage = 0;
-  for (; row < p.T; row += stride) {
-    Raw8<TX> raw[NV];
-    Lane<VEC> v[NV];
-    if constexpr (VEC == 8) {
-      fetch(row + (S - 1) * stride, stage == 0 ? S - 1 : stage - 1);
-      cp_async_wait<S - 1>();
-      const uint8_t* at = norm_smem + threadIdx.x * 16 + stage * (BYTES / 16) * piece;
+  if constexpr (VEC > 1)
+    for (int s = 0; s < S - 1; ++s) fetch(smem_u32(mine) + s * stage_bytes);
+  // VEC = 1: the next row's elements, in registers
+  float next[NV];
+  auto ahead = [&](int64_t r) {
+    if constexpr (VEC == 1) {
+      if (r >= p.T) return;
+      const TX* x = static_cast<const TX*>(p.x) + r * p.d;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        raw[i].clear();
-        if ((i * p.tpr + t) * VEC < p.d) raw[i].load_pieces(at + i * H * piece, piece);
-        raw[i].get(v[i]);
+        const float v = to_f32(x[on(i) ? col0 + i * step : 0]);
+        next[i] = on(i) ? v : 0.f;
       }
-      stage = stage + 1 == S ? 0 : stage + 1;
+    }
+  };
+  ahead(row);
+  // gamma and beta: the thread's columns in registers, or all in shared memory
+  uint8_t* const gs = norm_smem + S * stage_bytes;
+  uint8_t* const bs = gs + 4 * NV * step;
+  Lane<VEC> g[NV], b[NV];
+  if constexpr (STAGED) {
+    norm_stage_param<VEC>(p.gamma, p.param_f32, 1.f, p.d, NV * step, gs);
+    norm_stage_param<VEC>(p.beta, p.param_f32, 0.f, p.d, NV * step, bs);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      norm_param<VEC>(on(i) ? p.gamma : nullptr, p.param_f32, 1.f, col0 + i * step, g[i]);
+      norm_param<VEC>(on(i) ? p.beta : nullptr, p.param_f32, 0.f, col0 + i * step, b[i]);
+    }
+  }
+  __syncthreads();
+  const float n_lane = rg.on ? cols[rg.at] : 0.f;
+  uint32_t off = 0;  // of the current row's stage
+  TX* out = static_cast<TX*>(p.y) + row * p.d + col0;
+  for (; row < p.T; row += stride) {
+    Lane<VEC> v[NV];
+    uint32_t top[NV];
+    if constexpr (VEC > 1) {
+      fetch(smem_u32(mine) + (off == 0 ? (S - 1) * stage_bytes : off - stage_bytes));
+      cp_async_wait<S - 1>();
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        Raw<TX> raw;
+        raw.load(mine + off + i * piece);
+        raw.get(v[i]);
+        if constexpr (KEEP) top[i] = raw.top();
+      }
+      off = off == (S - 1) * stage_bytes ? 0 : off + stage_bytes;
     } else {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int col = i * p.tpr + t;
-        v[i].e[0] = col < p.d ? to_f32(static_cast<const TX*>(p.x)[row * p.d + col]) : 0.f;
-      }
+      for (int i = 0; i < NV; ++i) v[i].e[0] = next[i];
+      ahead(row + stride);
     }
 
     float mu = 0.f;
@@ -317,10 +398,11 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_fwd_kernel(const NormFwd p)
     E ss = both<E>(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if ((i * p.tpr + t) * VEC >= p.d) continue;
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        const E c = vsub(v[i].e[j], both<E>(mu));
+        E c = vsub(v[i].e[j], both<E>(mu));
+        if (VEC == 1) c = on(i) ? c : both<E>(0.f);
+        else if (i == NV - 1) c = vmul(c, both<E>(last));
         ss = vfma(c, c, ss);
       }
     }
@@ -328,16 +410,13 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_fwd_kernel(const NormFwd p)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
     if (rg.warps > 1) {
-      rg.put((threadIdx.x & 16) ? m2 : mu);
-      m2 = rg.get(1);
+      const float2 w = rg.exchange(mu, m2);
+      m2 = rg.on ? w.y : 0.f;
       if (center) {
-        const float muw = rg.get(0);
-        mu = rg.over_warps(muw * n_lane) * inv_d;
-        m2 = fmaf((muw - mu) * (muw - mu), n_lane, m2);
-        mu = __shfl_sync(0xffffffffu, mu, 0);
+        mu = rg.over_warps(w.x * n_lane) * inv_d;
+        m2 = fmaf((w.x - mu) * (w.x - mu), n_lane, m2);
       }
-      m2 = __shfl_sync(0xffffffffu, rg.over_warps(m2), 0);
-      rg.buf ^= 1;
+      m2 = rg.over_warps(m2);
     }
     const float rstd = rsqrtf(fmaf(m2, inv_d, p.eps));
     if (t == 0) {
@@ -347,33 +426,18 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_fwd_kernel(const NormFwd p)
 
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = (i * p.tpr + t) * VEC;
-      if (p.q) {
-        uint32_t top = 0;
-        if constexpr (VEC == 8) top = raw[i].top();
-        norm_keep8<VEC>(p, row, col, col < p.d, v[i], top);
-      }
-      if (col >= p.d) continue;
-      Lane<VEC> g, b;
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        g.e[j] = both<E>(1.f);
-        b.e[j] = both<E>(0.f);
-      }
-      if (VEC == 8 && p.staged) {
-        if constexpr (VEC == 8) {
-          if (p.gamma) norm_staged(gs, p.d, col, g);
-          if (p.beta) norm_staged(bs, p.d, col, b);
-        }
-      } else {
-        if (p.gamma) norm_param<VEC>(p.gamma, p.param_f32, col, g);
-        if (p.beta) norm_param<VEC>(p.beta, p.param_f32, col, b);
+      const int col = col0 + i * step;
+      if constexpr (KEEP) norm_keep8<VEC>(p, row, col, on(i), v[i], VEC > 1 ? top[i] : 0u);
+      if constexpr (STAGED) {
+        norm_staged<VEC>(gs, NV * step, col, g[i]);
+        norm_staged<VEC>(bs, NV * step, col, b[i]);
       }
 #pragma unroll
       for (int j = 0; j < N; ++j)
-        b.e[j] = vfma(vmul(vsub(v[i].e[j], both<E>(mu)), both<E>(rstd)), g.e[j], b.e[j]);
-      norm_store<TX, VEC>(static_cast<TX*>(p.y) + row * p.d + col, b);
+        v[i].e[j] = vfma(vmul(vsub(v[i].e[j], both<E>(mu)), both<E>(rstd)), g[i].e[j], b[i].e[j]);
+      if (on(i)) norm_store<TX, VEC>(out + i * step, v[i]);
     }
+    out += stride * p.d;
   }
 }
 
@@ -382,7 +446,7 @@ template <typename TX, int VEC>
 __global__ void __launch_bounds__(NORM_THREADS) norm_fwd_long_kernel(const NormFwd p) {
   using E = typename Lane<VEC>::E;
   constexpr int N = Lane<VEC>::N;
-  __shared__ float red[2][2][16];
+  __shared__ float2 red[2 * NORM_WARPS];
   RowGroup rg(red, NORM_THREADS);
   const float inv_d = 1.f / static_cast<float>(p.d);
   const int64_t span = static_cast<int64_t>(NORM_THREADS) * VEC;
@@ -421,8 +485,8 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_fwd_long_kernel(const NormF
 #pragma unroll
       for (int j = 0; j < N; ++j) v.e[j] = both<E>(0.f);
       uint32_t top = 0;
-      if constexpr (VEC == 8) {
-        Raw8<TX> r;
+      if constexpr (VEC > 1) {
+        Raw<TX> r;
         r.clear();
         if (on) r.load(x + c);
         r.get(v);
@@ -433,157 +497,192 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_fwd_long_kernel(const NormF
       if (p.q) norm_keep8<VEC>(p, row, c, on, v, top);
       if (!on) continue;
       Lane<VEC> g, b;
-      if (p.gamma) norm_param<VEC>(p.gamma, p.param_f32, c, g);
-      if (p.beta) norm_param<VEC>(p.beta, p.param_f32, c, b);
+      norm_param<VEC>(p.gamma, p.param_f32, 1.f, c, g);
+      norm_param<VEC>(p.beta, p.param_f32, 0.f, c, b);
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        v.e[j] = vmul(vsub(v.e[j], both<E>(mu)), both<E>(rstd));
-        if (p.gamma) v.e[j] = vmul(v.e[j], g.e[j]);
-        if (p.beta) v.e[j] = vadd(v.e[j], b.e[j]);
-      }
+      for (int j = 0; j < N; ++j)
+        v.e[j] = vfma(vmul(vsub(v.e[j], both<E>(mu)), both<E>(rstd)), g.e[j], b.e[j]);
       norm_store<TX, VEC>(static_cast<TX*>(p.y) + row * p.d + c, v);
     }
   }
 }
 
 // ------------------------------------------------------------------ backward
-template <typename TX, int VEC, int NV, bool Q8>
-__global__ void __launch_bounds__(NORM_THREADS) norm_bwd_kernel(const NormBwd p) {
+// NT: threads of a block, at most.  1024 of them (rows over 512 threads) have
+// 64 registers each, which hold the gradients' sums but not the row as well:
+// RELOAD reads it from shared memory a second time instead.
+template <typename TX, int VEC, int NV, bool Q8, bool STAGED, int NT>
+__global__ void __launch_bounds__(NT) norm_bwd_kernel(const NormBwd p) {
+  constexpr bool RELOAD = NT > NORM_THREADS;
   constexpr int BYTES = NORM_BWD_BYTES<TX, NV, Q8>;
-  constexpr int S = norm_stages(BYTES);
-  constexpr int H = sizeof(TX) / 2;  // 16-byte pieces of a vector
+  constexpr int S = VEC == 1 ? 1 : RELOAD ? 2 : norm_stages(BYTES, NT);
   using E = typename Lane<VEC>::E;
   constexpr int N = Lane<VEC>::N;
   extern __shared__ __align__(16) uint8_t norm_smem[];
-  __shared__ float red[2][2][16];
+  __shared__ float2 red[2 * NORM_WARPS];
   const int t = threadIdx.x % p.tpr, group = threadIdx.x / p.tpr, G = blockDim.x / p.tpr;
   RowGroup rg(red, p.tpr);
   const float inv_d = 1.f / static_cast<float>(p.d);
+  const int step = p.tpr * VEC;  // columns from a thread's vector to its next
+  const int col0 = t * VEC;
+  // only a thread's last vector may be past the row's end: dy and x are zeros
+  // there, which adds nothing to a sum
+  auto on = [&](int i) { return (VEC > 1 && i < NV - 1) || col0 + i * step < p.d; };
   Lane<VEC> dg[NV], db[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < N; ++j) dg[i].e[j] = db[i].e[j] = both<E>(0.f);
-  uint8_t* const gs = norm_smem + (VEC == 8 ? BYTES * S * blockDim.x : 0);
-  if (VEC == 8 && p.staged && p.gamma) norm_stage_param(p.gamma, p.param_f32, p.d, gs);
-  __syncthreads();
+  // a stage: dy's 16-byte pieces, then x's, or q's pieces of VEC bytes
+  const uint32_t piece = blockDim.x * 16, stage_bytes = BYTES * blockDim.x;
+  uint8_t* const mine = norm_smem + threadIdx.x * 16;
+  uint8_t* const mine8 = norm_smem + NV * piece + threadIdx.x * VEC;
+  uint8_t* const gs = norm_smem + S * stage_bytes;
 
-  // a stage: dy's pieces, then x's, or the 8-byte pieces of q
-  const uint32_t piece = blockDim.x * 16;
-  auto fetch = [&](int64_t row, int stage) {
-    if constexpr (VEC == 8) {
-      if (row < p.T) {
-        const uint32_t base = smem_u32(norm_smem) + stage * BYTES * blockDim.x;
-        const uint32_t at = base + threadIdx.x * 16;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * G;
+  int64_t row = static_cast<int64_t>(gridDim.x) * group + blockIdx.x;
+  int64_t row_in = row, at_in = row * p.d + col0;  // the next row to fetch, its first element
+  auto fetch = [&](uint32_t off) {
+    if constexpr (VEC > 1) {
+      if (row_in < p.T) {
+        const TX* dy = static_cast<const TX*>(p.dy) + at_in;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          const int col = (i * p.tpr + t) * VEC;
-          if (col >= p.d) continue;
-          const int64_t o = row * p.d + col;
-#pragma unroll
-          for (int h = 0; h < H; ++h) {
-            cp_async16(at + (i * H + h) * piece,
-                       reinterpret_cast<const uint8_t*>(static_cast<const TX*>(p.dy) + o) + 16 * h);
-            if constexpr (!Q8)
-              cp_async16(at + (NV * H + i * H + h) * piece,
-                         reinterpret_cast<const uint8_t*>(static_cast<const TX*>(p.x) + o) + 16 * h);
-          }
+          const int o = on(i) ? i * step : 0;
+          cp_async16(smem_u32(mine) + off + i * piece, dy + o, on(i) ? 16u : 0u);
           if constexpr (Q8)
-            cp_async8(base + NV * H * piece + (i * blockDim.x + threadIdx.x) * 8, p.q + o);
+            cp_async_bytes<VEC>(smem_u32(mine8) + off + i * blockDim.x * VEC, p.q + at_in + o,
+                                on(i) ? VEC : 0u);
+          else
+            cp_async16(smem_u32(mine) + off + (NV + i) * piece,
+                       static_cast<const TX*>(p.x) + at_in + o, on(i) ? 16u : 0u);
         }
+        row_in += stride;
+        at_in += stride * p.d;
       }
       cp_async_commit();
     }
   };
-  // what a row has besides: loaded a row ahead
+  // what a row has besides (VEC = 1: all of it): loaded a row ahead
   float mu_next = 0.f, rstd_next = 0.f;
+  float dy_next[NV], x_next[NV];
   uint32_t e_next[NV];
-  auto ahead = [&](int64_t row) {
-    if (row >= p.T) return;
-    if (p.mean) mu_next = p.mean[row];
-    rstd_next = p.rstd[row];
-    if constexpr (Q8 && VEC == 8) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i) e_next[i] = 133;
+  auto ahead = [&](int64_t r) {
+    if (r >= p.T) return;
+    if (p.mean) mu_next = p.mean[r];
+    rstd_next = p.rstd[r];
+    if constexpr (Q8 && VEC > 1) {
+      const uint8_t* e = p.e + r * p.groups + col0 / 32;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (on(i)) e_next[i] = e[i * (step / 32)];  // step is a multiple of 128
+    }
+    if constexpr (VEC == 1) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int col = (i * p.tpr + t) * VEC;
-        if (col < p.d) e_next[i] = p.e[row * p.groups + col / 32];
+        const int c = on(i) ? col0 + i * step : 0;
+        Lane<1> x;
+        norm_load_x<TX, 1, Q8>(p, r, c, x);
+        const float dy = to_f32(static_cast<const TX*>(p.dy)[r * p.d + c]);
+        x_next[i] = on(i) ? x.e[0] : 0.f;
+        dy_next[i] = on(i) ? dy : 0.f;
       }
     }
   };
-
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * G;
-  int64_t row = static_cast<int64_t>(gridDim.x) * group + blockIdx.x;
-  for (int s = 0; s < S - 1; ++s) fetch(row + s * stride, s);
+  if constexpr (VEC > 1)
+    for (int s = 0; s < S - 1; ++s) fetch(s * stage_bytes);
   ahead(row);
-  int stage = 0;
+  Lane<VEC> g1[NV];  // VEC = 1: the thread's columns of gamma
+  if constexpr (VEC == 1)
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      norm_param<VEC>(on(i) ? p.gamma : nullptr, p.param_f32, 1.f, col0 + i * step, g1[i]);
+  if constexpr (STAGED) {
+    norm_stage_param<VEC>(p.gamma, p.param_f32, 1.f, p.d, NV * step, gs);
+    __syncthreads();
+  }
+
+  uint32_t off = 0;  // of the current row's stage
+  TX* out = static_cast<TX*>(p.dx) + row * p.d + col0;
   for (; row < p.T; row += stride) {
     const float mu = mu_next, rstd = rstd_next;
     uint32_t e_row[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) e_row[i] = e_next[i];
-    ahead(row + stride);
-    const uint8_t* base = norm_smem + stage * BYTES * blockDim.x;
-    if constexpr (VEC == 8) {
-      fetch(row + (S - 1) * stride, stage == 0 ? S - 1 : stage - 1);
-      cp_async_wait<S - 1>();
-      stage = stage + 1 == S ? 0 : stage + 1;
-    }
     Lane<VEC> a[NV], xh[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      e_row[i] = e_next[i];
+      if constexpr (VEC == 1) {
+        a[i].e[0] = dy_next[i];
+        xh[i].e[0] = x_next[i];
+      }
+    }
+    ahead(row + stride);
+    if constexpr (VEC > 1) {
+      fetch(off == 0 ? (S - 1) * stage_bytes : off - stage_bytes);
+      cp_async_wait<S - 1>();
+    }
+    // dy, xh and gamma of vector i
+    auto get = [&](int i, Lane<VEC>& dy, Lane<VEC>& x, Lane<VEC>& g) {
+      if constexpr (VEC == 1) {
+        dy = a[i];
+        x = xh[i];
+        g = g1[i];
+      } else {
+        Raw<TX> r;
+        r.load(mine + off + i * piece);
+        r.get(dy);
+        if constexpr (Q8) {
+          Bytes<VEC> q;
+          q.load(mine8 + off + i * blockDim.x * VEC);
+          act8_unpack<VEC>(q, e_row[i], x);
+        } else {
+          r.load(mine + off + (NV + i) * piece);
+          r.get(x);
+        }
+        const int col = col0 + i * step;
+        if constexpr (STAGED) norm_staged<VEC>(gs, NV * step, col, g);
+        else norm_param<VEC>(on(i) ? p.gamma : nullptr, p.param_f32, 1.f, col, g);
+      }
+#pragma unroll
+      for (int j = 0; j < N; ++j) x.e[j] = vmul(vsub(x.e[j], both<E>(mu)), both<E>(rstd));
+    };
     E s1 = both<E>(0.f), s2 = both<E>(0.f);  // of a xh, of a
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = (i * p.tpr + t) * VEC;
-#pragma unroll
-      for (int j = 0; j < N; ++j) a[i].e[j] = xh[i].e[j] = both<E>(0.f);
-      if (col >= p.d) continue;
-      if constexpr (VEC == 8) {
-        Raw8<TX> r;
-        r.load_pieces(base + i * H * piece + threadIdx.x * 16, piece);
-        r.get(a[i]);
-        if constexpr (Q8) {
-          act8_unpack8(*reinterpret_cast<const uint2*>(base + NV * H * piece +
-                                                       (i * blockDim.x + threadIdx.x) * 8),
-                       e_row[i], xh[i]);
-        } else {
-          r.load_pieces(base + (NV + i) * H * piece + threadIdx.x * 16, piece);
-          r.get(xh[i]);
-        }
-      } else {
-        norm_load<TX, VEC>(static_cast<const TX*>(p.dy) + row * p.d + col, a[i]);
-        norm_load_x<TX, VEC, Q8>(p, row, col, xh[i]);
-      }
-      Lane<VEC> g;
-#pragma unroll
-      for (int j = 0; j < N; ++j) g.e[j] = both<E>(1.f);
-      if (p.gamma) {
-        if (VEC == 8 && p.staged) {
-          if constexpr (VEC == 8) norm_staged(gs, p.d, col, g);
-        } else {
-          norm_param<VEC>(p.gamma, p.param_f32, col, g);
-        }
-      }
+      Lane<VEC> dy, x, g;
+      get(i, dy, x, g);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        const E x = vmul(vsub(xh[i].e[j], both<E>(mu)), both<E>(rstd));
-        dg[i].e[j] = vfma(a[i].e[j], x, dg[i].e[j]);
-        db[i].e[j] = vadd(db[i].e[j], a[i].e[j]);
-        a[i].e[j] = vmul(a[i].e[j], g.e[j]);
-        s1 = vfma(a[i].e[j], x, s1);
-        s2 = vadd(s2, a[i].e[j]);
-        xh[i].e[j] = x;
+        dg[i].e[j] = vfma(dy.e[j], x.e[j], dg[i].e[j]);
+        db[i].e[j] = vadd(db[i].e[j], dy.e[j]);
+        const E ag = vmul(dy.e[j], g.e[j]);
+        s1 = vfma(ag, x.e[j], s1);
+        s2 = vadd(s2, ag);
+        if constexpr (!RELOAD) {
+          a[i].e[j] = ag;
+          xh[i].e[j] = x.e[j];
+        }
       }
     }
     const float2 c = rg.sum(vsum(s1), vsum(s2));
     const E c1 = both<E>(-c.x * inv_d), c2 = both<E>(p.mean ? c.y * inv_d : 0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = (i * p.tpr + t) * VEC;
-      if (col >= p.d) continue;
+      if constexpr (RELOAD) {
+        Lane<VEC> g;
+        get(i, a[i], xh[i], g);
+#pragma unroll
+        for (int j = 0; j < N; ++j) a[i].e[j] = vmul(a[i].e[j], g.e[j]);
+      }
 #pragma unroll
       for (int j = 0; j < N; ++j)
         a[i].e[j] = vmul(vfma(xh[i].e[j], c1, vsub(a[i].e[j], c2)), both<E>(rstd));
-      norm_store<TX, VEC>(static_cast<TX*>(p.dx) + row * p.d + col, a[i]);
+      if (on(i)) norm_store<TX, VEC>(out + i * step, a[i]);
     }
+    out += stride * p.d;
+    off = off == (S - 1) * stage_bytes ? 0 : off + stage_bytes;
   }
   if (!p.want_gamma && !p.want_beta) return;
   griddep_launch();  // norm_reduce_kernel may start; it waits for this kernel's end
@@ -594,16 +693,16 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_bwd_kernel(const NormBwd p)
   for (int k = 1; k < G; ++k) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = (i * p.tpr + t) * VEC;
-      if (group != k || col >= p.d) continue;
+      const int col = col0 + i * step;
+      if (group != k || !on(i)) continue;
       norm_store<float, VEC>(sums + col, dg[i]);
       norm_store<float, VEC>(sums + p.d + col, db[i]);
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = (i * p.tpr + t) * VEC;
-      if (group != 0 || col >= p.d) continue;
+      const int col = col0 + i * step;
+      if (group != 0 || !on(i)) continue;
       Lane<VEC> v;
       norm_load<float, VEC>(sums + col, v);
 #pragma unroll
@@ -618,8 +717,8 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_bwd_kernel(const NormBwd p)
   float* part = p.parts + static_cast<int64_t>(blockIdx.x) * 2 * p.d;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int col = (i * p.tpr + t) * VEC;
-    if (col >= p.d) continue;
+    const int col = col0 + i * step;
+    if (!on(i)) continue;
     if (p.want_gamma) norm_store<float, VEC>(part + col, dg[i]);
     if (p.want_beta) norm_store<float, VEC>(part + p.d + col, db[i]);
   }
@@ -630,7 +729,7 @@ template <typename TX, int VEC, bool Q8>
 __global__ void __launch_bounds__(NORM_THREADS) norm_bwd_long_kernel(const NormBwd p) {
   using E = typename Lane<VEC>::E;
   constexpr int N = Lane<VEC>::N;
-  __shared__ float red[2][2][16];
+  __shared__ float2 red[2 * NORM_WARPS];
   RowGroup rg(red, NORM_THREADS);
   const float inv_d = 1.f / static_cast<float>(p.d);
   const int64_t span = static_cast<int64_t>(NORM_THREADS) * VEC;
@@ -639,14 +738,13 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_bwd_long_kernel(const NormB
     auto load = [&](int64_t c, Lane<VEC>& a, Lane<VEC>& xh) {
       norm_load<TX, VEC>(static_cast<const TX*>(p.dy) + row * p.d + c, a);
       norm_load_x<TX, VEC, Q8>(p, row, c, xh);
-      if (p.gamma) {
-        Lane<VEC> g;
-        norm_param<VEC>(p.gamma, p.param_f32, c, g);
+      Lane<VEC> g;
+      norm_param<VEC>(p.gamma, p.param_f32, 1.f, c, g);
 #pragma unroll
-        for (int j = 0; j < N; ++j) a.e[j] = vmul(a.e[j], g.e[j]);
+      for (int j = 0; j < N; ++j) {
+        a.e[j] = vmul(a.e[j], g.e[j]);
+        xh.e[j] = vmul(vsub(xh.e[j], mu), rstd);
       }
-#pragma unroll
-      for (int j = 0; j < N; ++j) xh.e[j] = vmul(vsub(xh.e[j], mu), rstd);
     };
     E s1 = both<E>(0.f), s2 = both<E>(0.f);
     for (int64_t c = threadIdx.x * VEC; c < p.d; c += span) {
@@ -716,10 +814,10 @@ __global__ void __launch_bounds__(32 * NORM_COL_WARPS) norm_cols_kernel(const No
   }
 }
 
-constexpr int NORM_RED_COLS = 32, NORM_RED_ROWS = 16;
+constexpr int NORM_RED_COLS = 32, NORM_RED_ROWS = 32;
 
 // dgamma (blockIdx.y = 0) and dbeta (1): the sum of the blocks' parts, 32
-// columns a block, the parts shared by 16 threads a column.  Launched so that
+// columns a block, the parts shared by 32 threads a column.  Launched so that
 // it may start before the kernel that writes the parts has ended.
 __global__ void __launch_bounds__(NORM_RED_COLS* NORM_RED_ROWS)
 norm_reduce_kernel(const float* parts, int n, int32_t d, float* __restrict__ dgamma,
@@ -732,7 +830,7 @@ norm_reduce_kernel(const float* parts, int n, int32_t d, float* __restrict__ dga
   if (out == nullptr) return;
   float v = 0.f;
   if (col < d) {
-#pragma unroll 4
+#pragma unroll 8
     for (int k = r; k < n; k += NORM_RED_ROWS)
       v += parts[(static_cast<int64_t>(k) * 2 + blockIdx.y) * d + col];
   }

@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "../../include/ckl_ops.h"
 #include "ckl_act8.cuh"
@@ -56,27 +57,31 @@ bool act8_sizes_ok(int64_t T, int64_t d) {
 }
 
 template <typename TX>
-void act8_pack_launch(const void* x, int64_t T, int64_t d, int8_t* q, uint8_t* e, bool vec,
-                      int sms, cudaStream_t st) {
-  const int64_t groups = cdiv(d, 32);
-  const int64_t thr = T * groups * (vec ? 4 : 32);
+int act8_pack_launch(const void* x, int64_t T, int64_t d, int8_t* q, uint8_t* e, int sms,
+                     cudaStream_t st) {
+  constexpr int V = ckl::VEC16<TX>;
+  const bool vec = d % V == 0 && aligned(x, 16) && aligned(q, V);
+  const int64_t groups = cdiv(d, 32), thr = T * groups * (vec ? 32 / V : 32);
   const unsigned grid = static_cast<unsigned>(
       std::min<int64_t>(cdiv(thr, ckl::ACT8_THREADS), static_cast<int64_t>(sms) * 8));
-  auto* k = vec ? ckl::act8_pack_kernel<TX, true> : ckl::act8_pack_kernel<TX, false>;
+  auto* k = vec ? ckl::act8_pack_kernel<TX, V> : ckl::act8_pack_kernel<TX, 1>;
   k<<<grid, ckl::ACT8_THREADS, 0, st>>>(static_cast<const TX*>(x), T, static_cast<int32_t>(d),
                                         static_cast<int32_t>(groups), q, e);
+  return launched();
 }
 
 template <typename TX>
-void act8_unpack_launch(const int8_t* q, const uint8_t* e, int64_t T, int64_t d, void* x,
-                        bool vec, int sms, cudaStream_t st) {
-  const int64_t groups = cdiv(d, 32);
-  const int64_t thr = T * groups * (vec ? 4 : 32);
+int act8_unpack_launch(const int8_t* q, const uint8_t* e, int64_t T, int64_t d, void* x, int sms,
+                       cudaStream_t st) {
+  constexpr int V = ckl::VEC16<TX>;
+  const bool vec = d % V == 0 && aligned(x, 16) && aligned(q, V);
+  const int64_t groups = cdiv(d, 32), thr = T * groups * (vec ? 32 / V : 32);
   const unsigned grid = static_cast<unsigned>(
       std::min<int64_t>(cdiv(thr, ckl::ACT8_THREADS), static_cast<int64_t>(sms) * 8));
-  auto* k = vec ? ckl::act8_unpack_kernel<TX, true> : ckl::act8_unpack_kernel<TX, false>;
+  auto* k = vec ? ckl::act8_unpack_kernel<TX, V> : ckl::act8_unpack_kernel<TX, 1>;
   k<<<grid, ckl::ACT8_THREADS, 0, st>>>(q, e, T, static_cast<int32_t>(d),
                                         static_cast<int32_t>(groups), static_cast<TX*>(x));
+  return launched();
 }
 
 // How a norm's rows are taken: `vec` elements a load, `nv` vectors a thread,
@@ -85,23 +90,21 @@ struct NormShape {
   int vec, nv, tpr, threads;
 };
 
-// `want_nv` vectors a thread where a row has that many for two warps: what a
-// row costs a warp beside its elements (sums over lanes and warps, a barrier)
-// is then shared by more of them.  Four vectors where 512 threads need them, if
-// the kernel has that form (max_nv).
-NormShape norm_shape(int64_t d, bool vec, int want_nv, int max_nv) {
-  NormShape s{vec ? 8 : 1, 0, 0, 0};
-  const int64_t n = cdiv(d, s.vec);  // vectors of a row
-  if (n > static_cast<int64_t>(ckl::NORM_THREADS) * max_nv) return s;
-  if (!vec) s.nv = n <= ckl::NORM_THREADS * 8 ? 8 : 16;
-  else if (n > ckl::NORM_THREADS * want_nv) s.nv = 4;
-  else s.nv = n <= 32 ? 1 : n <= 64 ? 2 : want_nv;
-  s.tpr = static_cast<int>(cdiv(cdiv(n, s.nv), 32) * 32);
+// Rows of up to 512 threads with `want` vectors a thread; longer ones `more`
+// vectors (0: the kernels for long rows).  With the threads chosen first, only
+// a thread's last vector may be past the row's end.
+NormShape norm_shape(int64_t d, int vec, int want, int more) {
+  NormShape s{vec, 0, 0, 0};
+  const int64_t n = cdiv(d, vec);  // vectors of a row
+  const int nv = n <= static_cast<int64_t>(ckl::NORM_THREADS) * want ? want : more;
+  if (n > static_cast<int64_t>(ckl::NORM_THREADS) * nv) return s;
+  s.tpr = static_cast<int>(cdiv(n, 32 * nv) * 32);
+  s.nv = vec > 1 ? static_cast<int>(cdiv(n, s.tpr)) : nv;
   s.threads = ckl::NORM_THREADS / s.tpr * s.tpr;
   return s;
 }
 
-constexpr size_t kNormSmem = 220 * 1024;  // of a block, its ring and parameters
+constexpr size_t kNormSmem = 224 * 1024;  // of an SM, for the blocks' dynamic shared memory
 
 template <typename P>
 int norm_launch(void (*k)(P), const P& p, dim3 grid, int threads, size_t smem, cudaStream_t st) {
@@ -114,70 +117,105 @@ int norm_launch(void (*k)(P), const P& p, dim3 grid, int threads, size_t smem, c
   return launched();
 }
 
-template <typename TX>
-int norm_fwd_launch(const ckl::NormFwd& p, const NormShape& s, int sms, cudaStream_t st) {
-  using ckl::NORM_FWD_BYTES;
-  using ckl::norm_stages;
-  const int64_t rows = std::min<int64_t>(p.T, static_cast<int64_t>(sms) * 4);
-  if (s.nv == 0)
-    return norm_launch(s.vec == 8 ? ckl::norm_fwd_long_kernel<TX, 8>
-                                  : ckl::norm_fwd_long_kernel<TX, 1>,
-                       p, dim3(static_cast<unsigned>(rows)), ckl::NORM_THREADS, 0, st);
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(p.T, sms)));
-  auto go = [&](void (*k)(ckl::NormFwd), int bytes) {
-    const size_t ring = static_cast<size_t>(s.threads) * bytes * norm_stages(bytes);
-    const size_t params = static_cast<size_t>(p.d) * 4 * ((p.gamma != nullptr) + (p.beta != nullptr));
-    ckl::NormFwd f = p;
-    f.staged = p.T > sms && ring + params <= kNormSmem;
-    return norm_launch(k, f, grid, s.threads, f.staged ? ring + params : ring, st);
+template <int NV>
+using Nv = std::integral_constant<int, NV>;
+
+template <typename TX, bool KEEP>
+int norm_fwd_launch(const ckl::NormFwd& p0, bool vec, int sms, cudaStream_t st) {
+  constexpr int V = ckl::VEC16<TX>;
+  ckl::NormFwd p = p0;
+  // 16 elements a thread, 32 in long rows
+  const NormShape s = vec ? norm_shape(p.d, V, 16 / V, 32 / V) : norm_shape(p.d, 1, 8, 16);
+  p.tpr = s.tpr;
+  if (s.nv == 0) {
+    const unsigned rows = static_cast<unsigned>(std::min<int64_t>(p.T, sms * 4));
+    return norm_launch(vec ? ckl::norm_fwd_long_kernel<TX, V> : ckl::norm_fwd_long_kernel<TX, 1>, p,
+                       dim3(rows), ckl::NORM_THREADS, 0, st);
+  }
+  const dim3 one(static_cast<unsigned>(std::min<int64_t>(p.T, sms)));
+  const dim3 two(static_cast<unsigned>(std::min<int64_t>(p.T, 2 * sms)));
+  if (!vec)
+    return norm_launch(s.nv == 8 ? ckl::norm_fwd_kernel<TX, 1, 8, false, KEEP>
+                                 : ckl::norm_fwd_kernel<TX, 1, 16, false, KEEP>,
+                       p, two, s.threads, 0, st);
+  auto go = [&](auto nv) {
+    constexpr int NV = decltype(nv)::value, BYTES = ckl::NORM_FWD_BYTES<NV>;
+    if constexpr (NV * V <= 16) {
+      // the parameters in shared memory where two blocks' fit and groups have
+      // more than a row or two: 16384 x 4096 bf16 58 us with them in
+      // registers, 54 us so
+      const size_t smem = static_cast<size_t>(s.threads) * BYTES * ckl::norm_fwd_stages(BYTES) +
+                          static_cast<size_t>(s.tpr) * NV * V * 8;
+      if (p.T > 2 * sms && smem <= kNormSmem / 2)
+        return norm_launch(ckl::norm_fwd_kernel<TX, V, NV, true, KEEP>, p, two, s.threads, smem,
+                           st);
+    }
+    return norm_launch(
+        ckl::norm_fwd_kernel<TX, V, NV, false, KEEP>, p, one, s.threads,
+        static_cast<size_t>(s.threads) * BYTES * ckl::norm_stages(BYTES, ckl::NORM_THREADS), st);
   };
-  if (s.vec == 8)
-    return s.nv == 1   ? go(ckl::norm_fwd_kernel<TX, 8, 1>, NORM_FWD_BYTES<TX, 1>)
-           : s.nv == 2 ? go(ckl::norm_fwd_kernel<TX, 8, 2>, NORM_FWD_BYTES<TX, 2>)
-                       : go(ckl::norm_fwd_kernel<TX, 8, 4>, NORM_FWD_BYTES<TX, 4>);
-  return norm_launch(s.nv == 8 ? ckl::norm_fwd_kernel<TX, 1, 8> : ckl::norm_fwd_kernel<TX, 1, 16>,
-                     p, grid, s.threads, 0, st);
+  if constexpr (V == 4) {
+    if (s.nv == 8) return go(Nv<8>());
+    if (s.nv == 3) return go(Nv<3>());
+  }
+  return s.nv == 1 ? go(Nv<1>()) : s.nv == 2 ? go(Nv<2>()) : go(Nv<4>());
 }
 
 // Returns the status; `parts` is how many sums the workspace then holds.
 template <typename TX, bool Q8>
-int norm_bwd_launch(const ckl::NormBwd& p, const NormShape& s, int sms, cudaStream_t st,
-                    int& parts) {
-  using ckl::NORM_BWD_BYTES;
-  using ckl::norm_stages;
-  if (s.nv == 0) {
-    parts = static_cast<int>(std::min<int64_t>(cdiv(p.T, 8 * ckl::NORM_COL_WARPS), 64));
-    if (p.want_gamma || p.want_beta) {  // first: dx may take dy's place
-      const dim3 grid(static_cast<unsigned>(cdiv(p.d, 32 * s.vec)), static_cast<unsigned>(parts));
-      const int rc = norm_launch(s.vec == 8 ? ckl::norm_cols_kernel<TX, 8, Q8>
-                                            : ckl::norm_cols_kernel<TX, 1, Q8>,
-                                 p, grid, 32 * ckl::NORM_COL_WARPS, 0, st);
-      if (rc != CKL_OK) return rc;
-    }
-    return norm_launch(s.vec == 8 ? ckl::norm_bwd_long_kernel<TX, 8, Q8>
-                                  : ckl::norm_bwd_long_kernel<TX, 1, Q8>,
-                       p, dim3(static_cast<unsigned>(std::min<int64_t>(p.T, sms * 4))),
-                       ckl::NORM_THREADS, 0, st);
-  }
+int norm_bwd_launch(const ckl::NormBwd& p0, bool vec, int sms, cudaStream_t st, int& parts) {
+  constexpr int V = ckl::VEC16<TX>;
+  ckl::NormBwd p = p0;
+  const NormShape s = vec ? norm_shape(p.d, V, 16 / V, 0) : norm_shape(p.d, 1, 8, 16);
+  p.tpr = s.tpr;
   parts = static_cast<int>(std::min<int64_t>(p.T, std::min(sms, ckl::NORM_MAX_PARTS)));
   const dim3 grid(static_cast<unsigned>(parts));
   const size_t sums = static_cast<size_t>(p.d) * 8;  // a row group's, on the way to the first's
-  auto go = [&](void (*k)(ckl::NormBwd), int bytes) {
-    const size_t ring = static_cast<size_t>(s.threads) * bytes * norm_stages(bytes);
-    const size_t params = p.gamma ? static_cast<size_t>(p.d) * 4 : 0;
-    ckl::NormBwd f = p;
-    f.staged = p.T > sms && ring + params <= kNormSmem;
-    return norm_launch(k, f, grid, s.threads, std::max(f.staged ? ring + params : ring, sums), st);
+  auto go = [&](auto nv, auto threads, int tpr) {
+    constexpr int NV = decltype(nv)::value, NT = decltype(threads)::value;
+    constexpr int BYTES = ckl::NORM_BWD_BYTES<TX, NV, Q8>;
+    constexpr int S = NT > ckl::NORM_THREADS ? 2 : ckl::norm_stages(BYTES, NT);
+    const int block = NT / tpr * tpr;
+    const size_t ring = static_cast<size_t>(block) * BYTES * S;
+    const size_t params = static_cast<size_t>(tpr) * NV * V * 4;
+    if (p.T > 2 * sms && ring + params <= kNormSmem)
+      return norm_launch(ckl::norm_bwd_kernel<TX, V, NV, Q8, true, NT>, p, grid, block,
+                         std::max(ring + params, sums), st);
+    return norm_launch(ckl::norm_bwd_kernel<TX, V, NV, Q8, false, NT>, p, grid, block,
+                       std::max(ring, sums), st);
   };
-  if (s.vec == 8) {
-    if constexpr (sizeof(TX) == 2)
-      if (s.nv == 4) return go(ckl::norm_bwd_kernel<TX, 8, 4, Q8>, NORM_BWD_BYTES<TX, 4, Q8>);
-    return s.nv == 1 ? go(ckl::norm_bwd_kernel<TX, 8, 1, Q8>, NORM_BWD_BYTES<TX, 1, Q8>)
-                     : go(ckl::norm_bwd_kernel<TX, 8, 2, Q8>, NORM_BWD_BYTES<TX, 2, Q8>);
+  if (s.nv != 0 && !vec)
+    return norm_launch(s.nv == 8
+                           ? ckl::norm_bwd_kernel<TX, 1, 8, Q8, false, ckl::NORM_THREADS>
+                           : ckl::norm_bwd_kernel<TX, 1, 16, Q8, false, ckl::NORM_THREADS>,
+                       p, grid, s.threads, sums, st);
+  if (s.nv != 0) {
+    const Nv<ckl::NORM_THREADS> nt;
+    if constexpr (V == 4) {
+      if (s.nv == 3) return go(Nv<3>(), nt, s.tpr);
+      if (s.nv == 4) return go(Nv<4>(), nt, s.tpr);
+    }
+    return s.nv == 1 ? go(Nv<1>(), nt, s.tpr) : go(Nv<2>(), nt, s.tpr);
   }
-  return norm_launch(s.nv == 8 ? ckl::norm_bwd_kernel<TX, 1, 8, Q8>
-                               : ckl::norm_bwd_kernel<TX, 1, 16, Q8>,
-                     p, grid, s.threads, sums, st);
+  if constexpr (V == 8) {
+    if (vec && p.d <= 16384) {  // two vectors for each of up to 1024 threads
+      p.tpr = static_cast<int>(cdiv(p.d, 512) * 32);
+      return go(Nv<2>(), Nv<1024>(), p.tpr);
+    }
+  }
+  parts = static_cast<int>(std::min<int64_t>(cdiv(p.T, 8 * ckl::NORM_COL_WARPS), 64));
+  if (p.want_gamma || p.want_beta) {  // first: dx may take dy's place
+    const dim3 cols(static_cast<unsigned>(cdiv(p.d, 32 * (vec ? V : 1))),
+                    static_cast<unsigned>(parts));
+    const int rc = norm_launch(
+        vec ? ckl::norm_cols_kernel<TX, V, Q8> : ckl::norm_cols_kernel<TX, 1, Q8>, p, cols,
+        32 * ckl::NORM_COL_WARPS, 0, st);
+    if (rc != CKL_OK) return rc;
+  }
+  const unsigned rows = static_cast<unsigned>(std::min<int64_t>(p.T, sms * 4));
+  return norm_launch(
+      vec ? ckl::norm_bwd_long_kernel<TX, V, Q8> : ckl::norm_bwd_long_kernel<TX, 1, Q8>, p,
+      dim3(rows), ckl::NORM_THREADS, 0, st);
 }
 
 bool norm_sizes_ok(int64_t T, int64_t d) {
@@ -197,12 +235,9 @@ int ckl_act8_pack(const void* x, int32_t dtype, int64_t T, int64_t d, int8_t* q,
   if (const int rc = ops_device(dev)) return rc;
   if (T == 0) return CKL_OK;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool vec = d % 8 == 0 && aligned(x, 16) && aligned(q, 8);
-  if (dtype == CKL_DTYPE_F32)
-    act8_pack_launch<float>(x, T, d, q, exponents, vec, dev.sms, st);
-  else
-    act8_pack_launch<bf16>(x, T, d, q, exponents, vec, dev.sms, st);
-  return launched();
+  return dtype == CKL_DTYPE_F32
+             ? act8_pack_launch<float>(x, T, d, q, exponents, dev.sms, st)
+             : act8_pack_launch<bf16>(x, T, d, q, exponents, dev.sms, st);
 }
 
 int ckl_act8_unpack(const int8_t* q, const uint8_t* exponents, int64_t T, int64_t d, int32_t dtype,
@@ -214,12 +249,9 @@ int ckl_act8_unpack(const int8_t* q, const uint8_t* exponents, int64_t T, int64_
   if (const int rc = ops_device(dev)) return rc;
   if (T == 0) return CKL_OK;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool vec = d % 8 == 0 && aligned(x, 16) && aligned(q, 8);
-  if (dtype == CKL_DTYPE_F32)
-    act8_unpack_launch<float>(q, exponents, T, d, x, vec, dev.sms, st);
-  else
-    act8_unpack_launch<bf16>(q, exponents, T, d, x, vec, dev.sms, st);
-  return launched();
+  return dtype == CKL_DTYPE_F32
+             ? act8_unpack_launch<float>(q, exponents, T, d, x, dev.sms, st)
+             : act8_unpack_launch<bf16>(q, exponents, T, d, x, dev.sms, st);
 }
 
 int ckl_norm_forward(const void* x, int32_t dtype, const void* gamma, const void* beta,
@@ -237,9 +269,8 @@ int ckl_norm_forward(const void* x, int32_t dtype, const void* gamma, const void
   OpsDev dev;
   if (const int rc = ops_device(dev)) return rc;
   if (T == 0) return CKL_OK;
-  const bool vec = d % 8 == 0 && aligned(x, 16) && aligned(y, 16) && aligned(gamma, 16) &&
-                   aligned(beta, 16) && aligned(q, 8);
-  const NormShape s = norm_shape(d, vec, 4, vec ? 4 : 16);
+  const bool vec = d % static_cast<int64_t>(16 / eb) == 0 && aligned(x, 16) && aligned(y, 16) &&
+                   aligned(gamma, 16) && aligned(beta, 16) && aligned(q, 8);
   ckl::NormFwd p{};
   p.x = x;
   p.gamma = gamma;
@@ -252,12 +283,14 @@ int ckl_norm_forward(const void* x, int32_t dtype, const void* gamma, const void
   p.T = T;
   p.d = static_cast<int32_t>(d);
   p.groups = static_cast<int32_t>(cdiv(d, 32));
-  p.tpr = s.tpr;
   p.param_f32 = param_dtype == CKL_DTYPE_F32;
   p.eps = eps;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return dtype == CKL_DTYPE_F32 ? norm_fwd_launch<float>(p, s, dev.sms, st)
-                                : norm_fwd_launch<bf16>(p, s, dev.sms, st);
+  if (dtype == CKL_DTYPE_F32)
+    return q ? norm_fwd_launch<float, true>(p, vec, dev.sms, st)
+             : norm_fwd_launch<float, false>(p, vec, dev.sms, st);
+  return q ? norm_fwd_launch<bf16, true>(p, vec, dev.sms, st)
+           : norm_fwd_launch<bf16, false>(p, vec, dev.sms, st);
 }
 
 size_t ckl_norm_workspace_bytes(int64_t T, int64_t d) {
@@ -287,9 +320,8 @@ int ckl_norm_backward(const void* dy, int32_t dtype, const void* x, const int8_t
   if (const int rc = ops_device(dev)) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool q8 = x == nullptr;
-  const bool vec = d % 8 == 0 && aligned(dy, 16) && aligned(x, 16) && aligned(dx, 16) &&
+  const bool vec = d % static_cast<int64_t>(16 / eb) == 0 && aligned(dy, 16) && aligned(x, 16) && aligned(dx, 16) &&
                    aligned(gamma, 16) && (!q8 || aligned(q, 8));
-  const NormShape s = norm_shape(d, vec, 2, !vec ? 16 : dtype == CKL_DTYPE_F32 ? 2 : 4);
   int parts = 0;
   if (T > 0) {
     ckl::NormBwd p{};
@@ -305,16 +337,15 @@ int ckl_norm_backward(const void* dy, int32_t dtype, const void* x, const int8_t
     p.T = T;
     p.d = static_cast<int32_t>(d);
     p.groups = static_cast<int32_t>(cdiv(d, 32));
-    p.tpr = s.tpr;
     p.param_f32 = param_dtype == CKL_DTYPE_F32;
     p.want_gamma = dgamma != nullptr;
     p.want_beta = dbeta != nullptr;
     const int rc =
         dtype == CKL_DTYPE_F32
-            ? (q8 ? norm_bwd_launch<float, true>(p, s, dev.sms, st, parts)
-                  : norm_bwd_launch<float, false>(p, s, dev.sms, st, parts))
-            : (q8 ? norm_bwd_launch<bf16, true>(p, s, dev.sms, st, parts)
-                  : norm_bwd_launch<bf16, false>(p, s, dev.sms, st, parts));
+            ? (q8 ? norm_bwd_launch<float, true>(p, vec, dev.sms, st, parts)
+                  : norm_bwd_launch<float, false>(p, vec, dev.sms, st, parts))
+            : (q8 ? norm_bwd_launch<bf16, true>(p, vec, dev.sms, st, parts)
+                  : norm_bwd_launch<bf16, false>(p, vec, dev.sms, st, parts));
     if (rc != CKL_OK) return rc;
   }
   if (!grads) return CKL_OK;

@@ -46,8 +46,8 @@ enum {
  * ckl_act8_pack:   x [T, d] -> q [T, d], exponents [T, groups]
  * ckl_act8_unpack: q, exponents -> x [T, d]
  * T >= 0, 1 <= d < 2^31, T d < 2^62.  x aligned to its element.  Rows are taken 16
- * bytes at a time when d % 8 == 0, x is 16-byte and q 8-byte aligned, and an
- * element at a time otherwise; results are the same.
+ * bytes at a time when they are a multiple of that long and x is 16-byte and q
+ * 8-byte aligned, and an element at a time otherwise; results are the same.
  */
 CKL_API int ckl_act8_pack(const void* x, int32_t dtype, int64_t T, int64_t d, int8_t* q,
                           uint8_t* exponents, void* stream);
@@ -65,7 +65,8 @@ CKL_API int ckl_act8_unpack(const int8_t* q, const uint8_t* exponents, int64_t T
  *   q, exponents         out: x in 8 bits, for a backward that does not keep
  *                        x (ckl_act8_pack's result); both NULL = none
  * T >= 0, 1 <= d < 2^31 - 2^17, T d < 2^60, eps >= 0 and finite.  Arrays aligned to their elements; rows are taken 16 bytes at a time when
- * d % 8 == 0, x, y, gamma and beta are 16-byte and q 8-byte aligned.  y may be x.
+ * they are a multiple of that long and x, y, gamma and beta are 16-byte and q 8-byte
+ * aligned.  y may be x.
  */
 CKL_API int ckl_norm_forward(const void* x, int32_t dtype, const void* gamma, const void* beta,
                              int32_t param_dtype, int64_t T, int64_t d, float eps, void* y,
