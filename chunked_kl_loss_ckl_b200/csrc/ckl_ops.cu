@@ -218,6 +218,32 @@ int norm_bwd_launch(const ckl::NormBwd& p0, bool vec, int sms, cudaStream_t st, 
       dim3(rows), ckl::NORM_THREADS, 0, st);
 }
 
+#ifndef CKL_SAMPLE_PLACES
+#define CKL_SAMPLE_PLACES 2
+#endif
+template <int C>
+int sample_launch(const ckl::SampleParams& p, int sms, cudaStream_t st) {
+  const size_t smem = sizeof(ckl::SampleShared);
+  if (cudaFuncSetAttribute(ckl::sample_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem)) != cudaSuccess)
+    return CKL_ERR_CUDA;
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = C;
+  cluster.val.clusterDim.y = 1;
+  cluster.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(
+      std::min<int64_t>(p.T, std::max(1, sms * ckl::SM_BLOCKS / C)) * C));
+  cfg.blockDim = dim3(ckl::SM_THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &cluster;
+  cfg.numAttrs = C > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, ckl::sample_kernel<C>, p) == cudaSuccess ? CKL_OK
+                                                                         : CKL_ERR_CUDA;
+}
+
 bool norm_sizes_ok(int64_t T, int64_t d) {
   return T >= 0 && d >= 1 && d < kLim - 65536 && T < (int64_t(1) << 60) / d;
 }
@@ -403,14 +429,13 @@ int ckl_sample(const uint16_t* logits, int64_t ld, int64_t T, int64_t V, const f
   p.ids = ids;
   p.logp = logp;
   p.status = device_status;
-  const size_t smem = sizeof(ckl::SampleShared);
-  if (cudaFuncSetAttribute(ckl::sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess)
-    return CKL_ERR_CUDA;
-  const unsigned grid =
-      static_cast<unsigned>(std::min<int64_t>(T, static_cast<int64_t>(dev.sms) * 3));
-  ckl::sample_kernel<<<grid, ckl::SM_THREADS, smem, static_cast<cudaStream_t>(stream)>>>(p);
-  return launched();
+  // blocks a row: as many as keep all SMs' places filled
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int64_t places = static_cast<int64_t>(dev.sms) * CKL_SAMPLE_PLACES;
+  if (T * 8 <= places) return sample_launch<8>(p, dev.sms, st);
+  if (T * 4 <= places) return sample_launch<4>(p, dev.sms, st);
+  if (T * 2 <= places) return sample_launch<2>(p, dev.sms, st);
+  return sample_launch<1>(p, dev.sms, st);
 }
 
 }  // extern "C"

@@ -22,29 +22,50 @@
 // instead (sample_row_any), unless all of them are so far below the largest
 // logit (2^-64 of its weight) that their mass, under 2^-40 of the row's, is
 // never reached by a u of 24 bits.
+//
+// Bound by the adds to shared memory: 32 lanes' random bins meet 3.5 to a bank
+// on average, two cycles each, so 32 logits cost an SM 7 cycles where HBM brings
+// them in 2.7.  Few rows: a row is shared by a cluster of up to 8 blocks, which
+// count their parts, add each other's counters over distributed shared memory
+// and each look for the drawn value in their own part.
 #pragma once
 
 #include <cstdint>
 
 #include "ckl_bf16.cuh"
+#include "ckl_ptx.cuh"
 
 #define CKL_DEV_BAD_SAMPLE 16  // NaN or +inf logit, or a parameter or number out of range
 
 namespace ckl {
 
-constexpr int SM_THREADS = 512;
+#ifndef CKL_SM_THREADS
+#define CKL_SM_THREADS 512
+#endif
+#ifndef CKL_SM_BLOCKS
+#define CKL_SM_BLOCKS 2
+#endif
+constexpr int SM_THREADS = CKL_SM_THREADS;
+constexpr int SM_BLOCKS = CKL_SM_BLOCKS;        // of an SM, by their shared memory
 constexpr int SM_WARPS = SM_THREADS / 32;
+constexpr int SM_UNROLL = 4;                    // 16-byte loads a thread has under way
+constexpr int SM_MAX_CLUSTER = 8;
 constexpr uint32_t SM_LO = 0x2B80;              // bf16 bits of 2^-40
 constexpr uint32_t SM_HI = 0x4380;              // bf16 bits of 256
 constexpr int SM_HALF = SM_HI - SM_LO;          // bins of one sign
-constexpr int SM_BINS = 2 * SM_HALF + 1;
-constexpr int SM_CHUNKS = (SM_BINS + 31) / 32;  // 32 bins, one a lane
-constexpr int SM_SLOTS = SM_CHUNKS * 32;
+constexpr int SM_CB = 16;                       // bins of a chunk
+constexpr int SM_NEG = SM_HALF + SM_CB;         // first negative bin (zero has a chunk of its own)
+constexpr int SM_BINS = SM_NEG + SM_HALF;
+constexpr int SM_CHUNKS = SM_BINS / SM_CB;
+static_assert(SM_HALF % 128 == 0 && SM_LO % 128 == 0 && 128 % SM_CB == 0,
+              "a chunk's bins are of one binade");
 constexpr int SM_WIN = 8192;                    // keys of a window (rows of any values)
-constexpr int SM_ANY_CHUNKS = 65536 / 32;
+constexpr int SM_ANY_CB = 32;
+constexpr int SM_ANY_CHUNKS = 65536 / SM_ANY_CB;
 constexpr int SM_TILES = 1024;                  // tiles whose matches are counted, at most
 constexpr int SM_SEGS = 128;                    // parts of the row counted per draw
 constexpr int SM_BATCH = 64;                    // draws found in one pass
+static_assert(SM_BATCH <= SM_THREADS, "a draw a thread");
 
 struct SampleParams {
   const uint16_t* logits;
@@ -65,7 +86,7 @@ struct SampleParams {
 
 // A row's own parameters.
 struct SampleRow {
-  double temp, top_p, min_p;
+  double inv_temp, top_p, min_p;
   int32_t top_k;
   bool greedy, ok;
 };
@@ -73,44 +94,60 @@ struct SampleRow {
 struct alignas(16) SampleShared {
   // counters of the bins (slot order below), or of a window's keys; behind a
   // window's 8192 counters, the prefix masses of all 2048 chunks
-  uint32_t hist[SM_SLOTS];
+  uint32_t hist[SM_BINS];
   double pw[SM_CHUNKS + 1];    // mass before each chunk
+  double scan_w[SM_WARPS];
+  double mass;                 // what the filters keep
+  double draw_w;               // of the one draw
   uint32_t pc[SM_CHUNKS + 1];  // tokens before each chunk
+  uint32_t scan_c[SM_WARPS];
+  uint32_t kept;
   union {
-    uint16_t tiles[SM_TILES + 2];           // matches of one value in each tile
+    uint16_t tiles[SM_TILES];               // matches of one value in each tile
     uint32_t segs[SM_SEGS][SM_BATCH / 2];   // matches of up to 64 values in each part, 16 bits each
     uint32_t any_pc[SM_ANY_CHUNKS + 1];
   };
   uint32_t draw_bin[SM_BATCH], draw_rank[SM_BATCH];
-  uint32_t cb[32];  // one chunk's counters (rows of any values)
+  uint32_t drawn[65536 / 32];  // a bit for each bf16 pattern that was drawn
+  uint32_t found[SM_MAX_CLUSTER][SM_BATCH];  // matches of the drawn values in each block's part
+  uint32_t cb[SM_ANY_CB];  // one chunk's counters (rows of any values)
   float red[SM_WARPS];
   uint32_t flags[SM_WARPS];
+  float row_max;  // of this block's part
+  uint32_t row_flags;
+  SampleRow par;
 };
-static_assert(SM_WIN * 4 + (SM_ANY_CHUNKS + 1) * 8 <= SM_SLOTS * 4, "prefix masses behind a window");
+static_assert(SM_WIN * 4 + (SM_ANY_CHUNKS + 1) * 8 <= SM_BINS * 4, "prefix masses behind a window");
 
 enum : uint32_t { SF_BAD = 1, SF_LOW = 2, SF_ANY = 4 };
 
-// A row's elements: up to 7 before the first 16-byte boundary, whole vectors
-// of eight, up to 7 behind the last.
+// A row's elements: up to 7 before the first 16-byte boundary (the first
+// block's), whole vectors of eight, up to 7 behind the last (the last block's).
+// A block has vectors [0, nvec) of `v`.
 struct SampleSpan {
   const uint16_t* z;
   const uint4* v;
-  int head, nvec, tail;
-  __device__ __forceinline__ SampleSpan(const uint16_t* row, int V) : z(row) {
+  int head, first, nvec, tail, tail_at;
+  __device__ __forceinline__ SampleSpan(const uint16_t* row, int V, int blocks, int rank) : z(row) {
     const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) & 15u);
     head = min(V, static_cast<int>(((16u - off) & 15u) / 2u));
-    v = reinterpret_cast<const uint4*>(row + head);
-    nvec = (V - head) / 8;
-    tail = V - head - 8 * nvec;
+    const int all = (V - head) / 8;
+    const int per = ((all + blocks - 1) / blocks + 31) / 32 * 32;
+    const int v0 = min(all, rank * per);
+    nvec = min(all, v0 + per) - v0;
+    first = head + 8 * v0;  // id of the first vector's first element
+    v = reinterpret_cast<const uint4*>(row + head) + v0;
+    tail_at = head + 8 * all;
+    tail = rank == blocks - 1 ? V - tail_at : 0;
+    if (rank != 0) head = 0;
   }
-  __device__ __forceinline__ int tail_at() const { return head + 8 * nvec; }
 };
 
 // The counter of a value of the covered range: the positive values ascending,
-// zero, the negative ones descending (bits apart from the sign, plus SM_HALF
-// + 1 when it is set).
+// zero, the negative ones descending (bits apart from the sign, plus SM_NEG
+// when it is set).
 __device__ __forceinline__ uint32_t sample_slot(uint32_t x) {
-  return (x & 0x7FFFu) + (x >> 15) * (SM_HALF + 1) - SM_LO;
+  return (x & 0x7FFFu) + (x >> 15) * SM_NEG - SM_LO;
 }
 // Bin b (descending values) -> its counter, and its value.
 __device__ __forceinline__ int sample_bin_slot(int b) {
@@ -118,7 +155,7 @@ __device__ __forceinline__ int sample_bin_slot(int b) {
 }
 __device__ __forceinline__ uint32_t sample_bin_bits(int b) {
   if (b < SM_HALF) return SM_LO + (SM_HALF - 1 - b);
-  return b == SM_HALF ? 0u : 0x8000u + SM_LO + (b - SM_HALF - 1);
+  return b < SM_NEG ? 0u : 0x8000u + SM_LO + (b - SM_NEG);
 }
 // The bin whose counter a covered value or zero has.
 __device__ __forceinline__ int sample_slot_of(uint32_t x) {
@@ -149,46 +186,128 @@ __device__ __forceinline__ void sample_count1(uint32_t* hist, uint32_t x, uint32
   }
 }
 
+// Counts eight values, and keeps the largest of those seen.
+__device__ __forceinline__ void sample_count8(uint32_t* hist, const uint4& v, uint32_t& m2,
+                                              uint32_t& flags) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  m2 = bf16x2_max(m2, bf16x2_max(bf16x2_max(v.x, v.y), bf16x2_max(v.z, v.w)));
+  if ((sample_outside(v.x) | sample_outside(v.y) | sample_outside(v.z) | sample_outside(v.w)) ==
+      0u) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      atomicAdd(&hist[sample_slot(w[j] & 0xFFFFu)], 1u);
+      atomicAdd(&hist[sample_slot(w[j] >> 16)], 1u);
+    }
+  } else {
+    for (int j = 0; j < 4; ++j) {
+      sample_count1(hist, w[j] & 0xFFFFu, flags);
+      sample_count1(hist, w[j] >> 16, flags);
+    }
+  }
+}
+
+// The passes over a row are functions of their own, with few arguments, so
+// that what the rest of the kernel holds does not push their loads in flight
+// out of registers.
+//
+// Counts the vectors' values; returns the thread's packed maximum and, in the
+// high half, its flags.
+__device__ __noinline__ uint64_t sample_count_pass(uint32_t* hist, const uint4* __restrict__ z,
+                                                   int nvec) {
+  uint32_t flags = 0, m2 = 0xFF80FF80u;
+  int i = threadIdx.x;
+  for (; i + (SM_UNROLL - 1) * SM_THREADS < nvec; i += SM_UNROLL * SM_THREADS) {
+    uint4 v[SM_UNROLL];
+#pragma unroll
+    for (int k = 0; k < SM_UNROLL; ++k) v[k] = z[i + k * SM_THREADS];
+#pragma unroll
+    for (int k = 0; k < SM_UNROLL; ++k) sample_count8(hist, v[k], m2, flags);
+  }
+  for (; i < nvec; i += SM_THREADS) sample_count8(hist, z[i], m2, flags);
+  return m2 | (static_cast<uint64_t>(flags) << 32);
+}
+
+// Over 16 or 32 lanes.
+template <int W = 32>
 __device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 // Sum over the lanes up to and with this one.
-__device__ __forceinline__ double warp_scan(double v) {
-  const int lane = threadIdx.x & 31;
+template <int W = 32, typename T>
+__device__ __forceinline__ T warp_scan(T v) {
+  const int lane = threadIdx.x % W;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const double u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
-  }
-  return v;
-}
-__device__ __forceinline__ uint32_t warp_scan(uint32_t v) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
+  for (int o = 1; o < W; o <<= 1) {
+    const T u = __shfl_up_sync(0xffffffffu, v, o, W);
     if (lane >= o) v += u;
   }
   return v;
 }
 
 __device__ __forceinline__ double sample_weight(float v, float m, const SampleRow& r) {
-  return exp((static_cast<double>(v) - static_cast<double>(m)) / r.temp);
+  return exp((static_cast<double>(v) - static_cast<double>(m)) * r.inv_temp);
+}
+
+// Distributed shared memory of a cluster of C blocks: the address of a variable
+// of this block in another one, and a barrier of all threads of the cluster
+// (of the block where there is one).
+__device__ __forceinline__ uint32_t peer(const void* p, uint32_t rank) {
+  return mapa_shared(smem_u32(p), rank);
+}
+__device__ __forceinline__ uint32_t peer_load(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 peer_load4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void peer_store(uint32_t a, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ void peer_store(uint32_t a, double v) {
+  asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(a), "d"(v) : "memory");
+}
+template <int C>
+__device__ __forceinline__ void sync_all() {
+  if constexpr (C == 1) {
+    __syncthreads();
+  } else {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
 }
 
 // The counts of a row, read chunk by chunk: the bins of a row of covered
-// values, in shared memory.
+// values, in the shared memory of its C blocks.
+template <int C>
 struct SampleBins {
   SampleShared& sm;
-  static constexpr int CHUNKS = SM_CHUNKS, BINS = SM_BINS;
-  static constexpr bool BLOCK = false;  // a warp can read a chunk on its own
+  static constexpr int CHUNKS = SM_CHUNKS, BINS = SM_BINS, CB = SM_CB;
   __device__ __forceinline__ const double* pw() const { return sm.pw; }
   __device__ __forceinline__ const uint32_t* pc() const { return sm.pc; }
+  // of bin lane % CB of the chunk
   __device__ __forceinline__ uint32_t count(int chunk) const {
-    const int b = chunk * 32 + (threadIdx.x & 31);
-    return b < SM_BINS ? sm.hist[sample_bin_slot(b)] : 0u;
+    return count_of(chunk * CB + threadIdx.x % CB);
+  }
+  // from a chunk's bin to its next, in value
+  __device__ __forceinline__ double gap(int chunk) const {
+    return static_cast<double>(value(chunk * CB + 1)) - static_cast<double>(value(chunk * CB));
+  }
+  __device__ __forceinline__ uint32_t count_of(int b) const {
+    const uint32_t* at = &sm.hist[sample_bin_slot(b)];
+    if constexpr (C == 1) return *at;
+    uint32_t n = 0;
+#pragma unroll
+    for (int r = 0; r < C; ++r) n += peer_load(peer(at, r));
+    return n;
   }
   __device__ __forceinline__ float value(int b) const { return bf16_value(sample_bin_bits(b)); }
 };
@@ -200,22 +319,21 @@ struct SampleKeys {
   const uint16_t* z;
   int V;
   // bins up to that of -inf; behind it come the keys of NaNs
-  static constexpr int CHUNKS = SM_ANY_CHUNKS, BINS = 0xFF81;
-  static constexpr bool BLOCK = true;
+  static constexpr int CHUNKS = SM_ANY_CHUNKS, BINS = 0xFF81, CB = SM_ANY_CB;
   __device__ __forceinline__ double* pw() const {
     return reinterpret_cast<double*>(sm.hist + SM_WIN);
   }
   __device__ __forceinline__ uint32_t* pc() const { return sm.any_pc; }
   __device__ __noinline__ uint32_t count(int chunk) const {
     __syncthreads();
-    if (threadIdx.x < 32) sm.cb[threadIdx.x] = 0;
+    if (threadIdx.x < CB) sm.cb[threadIdx.x] = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < V; i += SM_THREADS) {
       const uint32_t b = 0xFFFFu - bf16_key(z[i]);
-      if (static_cast<int>(b >> 5) == chunk && z[i] != 0xFF80u) atomicAdd(&sm.cb[b & 31u], 1u);
+      if (static_cast<int>(b / CB) == chunk && z[i] != 0xFF80u) atomicAdd(&sm.cb[b % CB], 1u);
     }
     __syncthreads();
-    return sm.cb[threadIdx.x & 31];
+    return sm.cb[threadIdx.x % CB];
   }
   __device__ __forceinline__ float value(int b) const {
     return key_value(0xFFFFu - static_cast<uint32_t>(b));
@@ -232,15 +350,18 @@ struct SamplePlace {
   double w;     // of one token of the bin
 };
 
-// The last chunk c with pred(prefix c); pred holds for the first one and
-// changes once.
+// The last of entries 0 .. n - 1 with pred; pred holds for the first one and
+// changes once.  32 entries are tried at a time.
 template <typename F>
 __device__ __forceinline__ int sample_chunk(int n, F&& pred) {
-  int lo = 0, hi = n;  // pred(lo), not pred(hi)
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (pred(mid)) lo = mid;
-    else hi = mid;
+  int lo = 0, size = n;  // the answer is in [lo, lo + size)
+  while (size > 1) {
+    const int step = (size + 31) / 32;
+    const int i = lo + static_cast<int>(threadIdx.x & 31) * step;
+    const bool yes = i < lo + size && pred(i);
+    const int k = __popc(__ballot_sync(0xffffffffu, yes)) - 1;  // lane 0's holds
+    size = min(step, lo + size - (lo + k * step));
+    lo += k * step;
   }
   return lo;
 }
@@ -249,16 +370,16 @@ __device__ __forceinline__ int sample_chunk(int n, F&& pred) {
 template <typename S>
 __device__ __forceinline__ SamplePlace sample_at_rank(const S& s, float m, const SampleRow& r,
                                                       uint32_t rank) {
+  constexpr int CB = S::CB;
   const int c = sample_chunk(S::CHUNKS, [&](int i) { return s.pc()[i] <= rank; });
-  const int lane = threadIdx.x & 31;
   const uint32_t n = s.count(c);
-  const double w = n ? sample_weight(s.value(c * 32 + lane), m, r) : 0.0;
-  const uint32_t upto = warp_scan(n) + s.pc()[c];
-  const double mass = warp_scan(n * w) - n * w + s.pw()[c];
+  const double w = n ? sample_weight(s.value(c * CB + threadIdx.x % CB), m, r) : 0.0;
+  const uint32_t upto = warp_scan<CB>(n) + s.pc()[c];
+  const double mass = warp_scan<CB>(n * w) - n * w + s.pw()[c];
   const uint32_t hit = __ballot_sync(0xffffffffu, upto > rank);
-  const int l = hit ? __ffs(hit) - 1 : 31;
+  const int l = hit ? __ffs(hit) - 1 : CB - 1;
   SamplePlace p;
-  p.bin = c * 32 + l;
+  p.bin = c * CB + l;
   const uint32_t before = __shfl_sync(0xffffffffu, upto - n, l);
   p.in_bin = rank - before;
   p.rank = rank;
@@ -271,20 +392,21 @@ __device__ __forceinline__ SamplePlace sample_at_rank(const S& s, float m, const
 template <bool STRICT, typename S>
 __device__ __forceinline__ SamplePlace sample_at_mass(const S& s, float m, const SampleRow& r,
                                                       double target) {
+  constexpr int CB = S::CB;
   auto past = [&](double x) { return STRICT ? x > target : x >= target; };
   const int c = sample_chunk(S::CHUNKS, [&](int i) { return i == 0 || !past(s.pw()[i]); });
-  const int lane = threadIdx.x & 31;
   const uint32_t n = s.count(c);
-  const double w = n ? sample_weight(s.value(c * 32 + lane), m, r) : 0.0;
-  const uint32_t rank0 = warp_scan(n) - n + s.pc()[c];
-  const double upto = warp_scan(n * w) + s.pw()[c];
-  const uint32_t some = __ballot_sync(0xffffffffu, n > 0);
-  const uint32_t hit = __ballot_sync(0xffffffffu, n > 0 && past(upto));
+  const double w = n ? sample_weight(s.value(c * CB + threadIdx.x % CB), m, r) : 0.0;
+  const uint32_t rank0 = warp_scan<CB>(n) - n + s.pc()[c];
+  const double upto = warp_scan<CB>(n * w) + s.pw()[c];
+  constexpr uint32_t LANES = CB == 32 ? 0xffffffffu : (1u << CB) - 1u;  // lanes of one copy
+  const uint32_t some = __ballot_sync(0xffffffffu, n > 0) & LANES;
+  const uint32_t hit = __ballot_sync(0xffffffffu, n > 0 && past(upto)) & LANES;
   // sums taken in another order may differ in the last bit: then the chunk's last
   const int l = hit ? __ffs(hit) - 1 : (some ? 31 - __clz(some) : 0);
   const uint32_t nl = __shfl_sync(0xffffffffu, n, l);
   SamplePlace p;
-  p.bin = c * 32 + l;
+  p.bin = c * CB + l;
   p.w = __shfl_sync(0xffffffffu, w, l);
   const double before = __shfl_sync(0xffffffffu, upto - n * w, l);
   const double x = (target - before) / p.w;  // tokens of the bin before the target
@@ -314,35 +436,39 @@ __device__ __forceinline__ uint32_t sample_min_p(const S& s, float m, const Samp
     hi = min(hi, last + step);
     lo = last + 1;
   }
-  if (lo >= S::BINS) return s.pc()[S::CHUNKS];
-  const uint32_t n = s.count(lo / 32);
-  const uint32_t in = __reduce_add_sync(0xffffffffu, lane < (lo & 31) ? n : 0u);
-  return s.pc()[lo / 32] + in;
+  if (lo >= S::CHUNKS * S::CB) return s.pc()[S::CHUNKS];
+  const uint32_t n = s.count(lo / S::CB);
+  const uint32_t in = __reduce_add_sync(0xffffffffu, lane < lo % S::CB ? n : 0u);
+  return s.pc()[lo / S::CB] + in;
 }
 
 // How many tokens the filters keep and their mass.
 template <typename S>
-__device__ __forceinline__ uint32_t sample_kept(const S& s, float m, const SampleRow& r,
+__device__ __noinline__ uint32_t sample_kept(const S& s, float m, const SampleRow& r,
                                                 double& mass) {
-  const uint32_t n = s.pc()[S::CHUNKS];
-  uint32_t L = n;
+  uint32_t L = s.pc()[S::CHUNKS];
   mass = s.pw()[S::CHUNKS];
-  if (r.greedy) {
-    L = 1;
-  } else {
-    if (r.top_k > 0 && static_cast<uint32_t>(r.top_k) < n) {
-      L = static_cast<uint32_t>(r.top_k);
-      const SamplePlace p = sample_at_rank(s, m, r, L - 1);
-      mass = p.mass + p.w;
-    }
-    uint32_t keep = L;
-    if (r.top_p < 1.0) keep = min(keep, sample_at_mass<false>(s, m, r, r.top_p * mass).rank + 1);
-    if (r.min_p > 0.0) keep = min(keep, max(1u, sample_min_p(s, m, r)));
-    if (keep == L) return L;
-    L = keep;
+  uint32_t cut = r.greedy ? 1u : r.top_k > 0 ? static_cast<uint32_t>(r.top_k) : L;
+  if (cut < L) {
+    L = cut;
+    const SamplePlace p = sample_at_rank(s, m, r, L - 1);
+    mass = p.mass + p.w;
   }
-  const SamplePlace p = sample_at_rank(s, m, r, L - 1);
-  mass = p.mass + p.w;
+  if (r.greedy) return L;
+  cut = L;
+  if (r.min_p > 0.0) cut = max(1u, sample_min_p(s, m, r));
+  if (r.top_p < 1.0) {
+    const SamplePlace p = sample_at_mass<false>(s, m, r, r.top_p * mass);
+    if (p.rank < L && p.rank < cut) {
+      mass = p.mass + p.w;
+      return p.rank + 1;
+    }
+  }
+  if (cut < L) {
+    L = cut;
+    const SamplePlace p = sample_at_rank(s, m, r, L - 1);
+    mass = p.mass + p.w;
+  }
   return L;
 }
 
@@ -351,27 +477,83 @@ template <typename S>
 __device__ __forceinline__ SamplePlace sample_draw(const S& s, float m, const SampleRow& r,
                                                    uint32_t L, double mass, float u) {
   const SamplePlace p = sample_at_mass<true>(s, m, r, static_cast<double>(u) * mass);
-  return p.rank < L ? p : sample_at_rank(s, m, r, L - 1);  // u mass rounded up to the mass
+  // rounding may leave the kept tokens, or a chunk's
+  return p.rank < L && p.w > 0.0 ? p : sample_at_rank(s, m, r, min(p.rank, L - 1));
+}
+
+// A draw a lane, among the first L tokens: the chunk by bisection, then its
+// bins one after another, weights as a geometric series (SampleBins only).
+template <typename S>
+__device__ __forceinline__ SamplePlace sample_draw_lane(const S& s, float m, const SampleRow& r,
+                                                        uint32_t L, double mass, float u) {
+  const double target = static_cast<double>(u) * mass;
+  int c = 0, hi = S::CHUNKS;  // pw[c] <= target
+  while (hi - c > 1) {
+    const int mid = (c + hi) / 2;
+    if (s.pw()[mid] <= target) c = mid;
+    else hi = mid;
+  }
+  const int b0 = c * S::CB;
+  const double gap = s.gap(c) * r.inv_temp;  // <= 0: from a bin to the next
+  const bool series = gap > -20.0;
+  double w = series ? sample_weight(s.value(b0), m, r) : 0.0;
+  const double ratio = exp(gap);
+  SamplePlace p;
+  p.bin = b0;
+  p.in_bin = 0;
+  p.mass = s.pw()[c];
+  p.rank = s.pc()[c];  // of the bin's first token
+  double before = p.mass;
+  uint32_t rank = p.rank;
+#pragma unroll 1
+  for (int k = 0; k < S::CB; ++k) {
+    const uint32_t n = s.count_of(b0 + k);
+    if (n) {
+      p.bin = b0 + k;
+      p.rank = rank;
+      p.mass = before;
+      p.in_bin = n;  // for now, its tokens
+      rank += n;
+      before += n * (series ? w : sample_weight(s.value(b0 + k), m, r));
+      if (before > target) break;
+    }
+    w *= ratio;
+  }
+  p.w = sample_weight(s.value(p.bin), m, r);
+  double j = floor((target - p.mass) / p.w);
+  j = fmin(fmax(j, 0.0), p.in_bin ? p.in_bin - 1.0 : 0.0);
+  if (p.rank + j >= L) j = fmax(0.0, static_cast<double>(L) - 1.0 - p.rank);  // rounding
+  p.in_bin = static_cast<uint32_t>(j);
+  return p;
 }
 
 __device__ __forceinline__ bool sample_u_ok(float u) { return u >= 0.f && u < 1.f; }
 
-// Turns the chunks' counts and masses into those before each chunk (one warp).
-__device__ __forceinline__ void sample_prefix(uint32_t* pc, double* pw, int n) {
-  const int lane = threadIdx.x & 31;
-  const int per = (n + 31) / 32, b = min(n, lane * per), e = min(n, b + per);
+// Turns the chunks' counts and masses into those before each chunk (the block).
+__device__ __forceinline__ void sample_prefix(SampleShared& sm, uint32_t* pc, double* pw, int n) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per = (n + SM_THREADS - 1) / SM_THREADS;
+  const int b = min(n, static_cast<int>(threadIdx.x) * per), e = min(n, b + per);
   uint32_t c = 0;
   double w = 0.0;
   for (int i = b; i < e; ++i) {
     c += pc[i];
     w += pw[i];
   }
-  uint32_t c0 = warp_scan(c) - c;
-  double w0 = warp_scan(w) - w;
+  uint32_t c0 = warp_scan(c);
+  double w0 = warp_scan(w);
   if (lane == 31) {
-    pc[n] = c0 + c;
-    pw[n] = w0 + w;
+    sm.scan_c[warp] = c0;
+    sm.scan_w[warp] = w0;
   }
+  __syncthreads();
+  // every warp scans the warps' sums for itself
+  const uint32_t ca = lane < SM_WARPS ? sm.scan_c[lane] : 0u;
+  const double wa = lane < SM_WARPS ? sm.scan_w[lane] : 0.0;
+  const uint32_t cu = warp_scan(ca);
+  const double wu = warp_scan(wa);
+  c0 += __shfl_sync(0xffffffffu, cu - ca, warp) - c;
+  w0 = __shfl_sync(0xffffffffu, wu - wa, warp) + (w0 - w);
   for (int i = b; i < e; ++i) {
     const uint32_t ci = pc[i];
     const double wi = pw[i];
@@ -380,6 +562,11 @@ __device__ __forceinline__ void sample_prefix(uint32_t* pc, double* pw, int n) {
     c0 += ci;
     w0 += wi;
   }
+  if (threadIdx.x == SM_THREADS - 1) {  // lane 31: the sum over all warps
+    pc[n] = cu;
+    pw[n] = wu;
+  }
+  __syncthreads();
 }
 
 // A value to look for among packed bf16 pairs (zero: of either sign).
@@ -403,36 +590,43 @@ struct SampleMatch {
 };
 constexpr uint32_t SM_EIGHT = 0xF000F000u;
 
-// Id of occurrence `rank` (from 0) of a value, by one warp over vectors
-// [v0, v1) of the row; before them come `rank` of its occurrences fewer.
-// Returns -1 if they are not there.
+// Id of occurrence `rank` (from 0) of a value among vectors [v0, v1) of the
+// row, by one warp, four loads under way.  Returns -1 if it is not there.
 __device__ __forceinline__ int sample_scan(const SampleSpan& sp, const SampleMatch& mt, int v0,
                                            int v1, uint32_t rank) {
   const int lane = threadIdx.x & 31;
-  for (int b = v0; b < v1; b += 32) {
-    uint32_t no = SM_EIGHT;
-    if (b + lane < v1) no = mt.differs8(sp.v[b + lane]);
-    const uint32_t n = 8u - __popc(no);
-    const uint32_t upto = warp_scan(n);
-    const uint32_t all = __shfl_sync(0xffffffffu, upto, 31);
-    if (rank >= all) {
-      rank -= all;
-      continue;
-    }
-    const uint32_t hit = __ballot_sync(0xffffffffu, upto > rank);
-    const int l = __ffs(hit) - 1;
-    int id = 0;
-    if (lane == l) {
-      uint32_t left = rank - (upto - n);
-      for (int j = 0; j < 8; ++j) {
-        const bool is = !((no >> ((j & 1) ? 31 - j / 2 : 15 - j / 2)) & 1u);
-        if (is && left-- == 0) {
-          id = sp.head + 8 * (b + lane) + j;
-          break;
+  for (int b = v0; b < v1; b += 32 * SM_UNROLL) {
+    uint4 v[SM_UNROLL];
+    uint32_t no[SM_UNROLL];
+#pragma unroll
+    for (int k = 0; k < SM_UNROLL; ++k)
+      if (b + k * 32 + lane < v1) v[k] = sp.v[b + k * 32 + lane];
+#pragma unroll
+    for (int k = 0; k < SM_UNROLL; ++k)
+      no[k] = b + k * 32 + lane < v1 ? mt.differs8(v[k]) : SM_EIGHT;
+#pragma unroll
+    for (int k = 0; k < SM_UNROLL; ++k) {
+      const uint32_t n = 8u - __popc(no[k]);
+      const uint32_t all = __reduce_add_sync(0xffffffffu, n);
+      if (rank >= all) {
+        rank -= all;
+        continue;
+      }
+      const uint32_t upto = warp_scan(n);
+      const int l = __ffs(__ballot_sync(0xffffffffu, upto > rank)) - 1;
+      int id = 0;
+      if (lane == l) {
+        uint32_t left = rank - (upto - n);
+        for (int j = 0; j < 8; ++j) {
+          const bool is = !((no[k] >> ((j & 1) ? 31 - j / 2 : 15 - j / 2)) & 1u);
+          if (is && left-- == 0) {
+            id = sp.first + 8 * (b + k * 32 + lane) + j;
+            break;
+          }
         }
       }
+      return __shfl_sync(0xffffffffu, id, l);
     }
-    return __shfl_sync(0xffffffffu, id, l);
   }
   return -1;
 }
@@ -453,42 +647,97 @@ __device__ __forceinline__ int sample_scan_few(const SampleSpan& sp, const Sampl
   return at + __ffs(__ballot_sync(0xffffffffu, me)) - 1;
 }
 
-// Id of one (value, occurrence), by the block: the matches of every tile of
-// the row are counted, and the tile that holds the occurrence is read again.
-// The result is valid in warp 0.
-__device__ int sample_find(SampleShared& sm, const SampleSpan& sp, uint32_t bits, uint32_t rank) {
+// The matches of a value in each tile of `steps` x 32 vectors; returns those in
+// the warp's tiles.
+__device__ __noinline__ uint32_t sample_tiles_pass(uint16_t* tiles, const uint4* __restrict__ z,
+                                                   int nvec, int steps, uint32_t bits) {
+  const SampleMatch mt(bits);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tv = 32 * steps, nt = (nvec + tv - 1) / tv;
+  uint32_t mine = 0;
+  int t = warp;
+  if (steps == 1) {  // whole tiles, SM_UNROLL loads under way
+    for (; t + (SM_UNROLL - 1) * SM_WARPS < nvec / 32; t += SM_UNROLL * SM_WARPS) {
+      uint4 v[SM_UNROLL];
+#pragma unroll
+      for (int k = 0; k < SM_UNROLL; ++k) v[k] = z[(t + k * SM_WARPS) * 32 + lane];
+#pragma unroll
+      for (int k = 0; k < SM_UNROLL; ++k) {
+        const uint32_t n = __reduce_add_sync(0xffffffffu, 8u - __popc(mt.differs8(v[k])));
+        if (lane == 0) tiles[t + k * SM_WARPS] = static_cast<uint16_t>(n);
+        mine += n;
+      }
+    }
+  }
+  for (; t < nt; t += SM_WARPS) {
+    uint32_t n = 0;
+    for (int s = 0; s < steps; ++s) {
+      const int i = t * tv + s * 32 + lane;
+      if (i < nvec) n += 8u - __popc(mt.differs8(z[i]));
+    }
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) tiles[t] = static_cast<uint16_t>(n);
+    mine += n;
+  }
+  return mine;
+}
+
+// Writes the id of one (value, occurrence): the matches in every tile of the
+// block's part are counted, the blocks' counts joined, and the tile that holds
+// the occurrence is read again by the first warp of the block that has it.
+template <int C>
+__device__ __forceinline__ void sample_find(SampleShared& sm, const SampleSpan& sp, uint32_t rank0,
+                                            uint32_t bits, uint32_t rank, int32_t* id_out) {
   const SampleMatch mt(bits);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int steps = max(1, (sp.nvec + 32 * SM_TILES - 1) / (32 * SM_TILES));  // 32 vectors each
   const int tv = 32 * steps, nt = (sp.nvec + tv - 1) / tv;
-  __syncthreads();  // the counters of tiles share memory with what was read before
-  for (int t = warp; t < nt; t += SM_WARPS) {
-    uint32_t n = 0;
-    for (int k = 0; k < steps; ++k) {
-      const int i = t * tv + k * 32 + lane;
-      if (i < sp.nvec) n += 8u - __popc(mt.differs8(sp.v[i]));
+  const uint32_t mine = sample_tiles_pass(sm.tiles, sp.v, sp.nvec, steps, bits);
+  if constexpr (C > 1) {
+    if (lane == 0) sm.scan_c[warp] = mine;
+    __syncthreads();
+    if (warp == 0) {
+      uint32_t all = __reduce_add_sync(0xffffffffu, lane < SM_WARPS ? sm.scan_c[lane] : 0u);
+      const bool few = lane < sp.head ? mt.is(sp.z[lane])
+                                      : lane < sp.head + sp.tail &&
+                                            mt.is(sp.z[sp.tail_at + lane - sp.head]);
+      all += __popc(__ballot_sync(0xffffffffu, few));
+      if (lane < C) peer_store(peer(&sm.found[rank0][0], lane), all);
     }
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (lane == 0) sm.tiles[t] = static_cast<uint16_t>(n);
+    sync_all<C>();
+  } else {
+    __syncthreads();
   }
-  __syncthreads();
-  if (warp != 0) return -1;
-  const int few = sample_scan_few(sp, mt, 0, sp.head, rank);
-  if (few >= 0) return few;
-  const int per = (nt + 31) / 32;
-  uint32_t mine = 0;
-  for (int i = lane * per; i < min(nt, (lane + 1) * per); ++i) mine += sm.tiles[i];
-  const uint32_t upto = warp_scan(mine);
-  const uint32_t hit = __ballot_sync(0xffffffffu, upto > rank);
-  if (hit == 0) {
-    rank -= __shfl_sync(0xffffffffu, upto, 31);
-    return sample_scan_few(sp, mt, sp.tail_at(), sp.tail, rank);
+  if (warp != 0) return;
+  if constexpr (C > 1) {
+    uint32_t here = 0;
+    for (uint32_t k = 0; k <= rank0; ++k) {
+      here = sm.found[k][0];
+      if (k == rank0) break;
+      if (rank < here) return;  // in a block before this one
+      rank -= here;
+    }
+    if (rank >= here) return;
   }
-  const int l = __ffs(hit) - 1;
-  rank -= __shfl_sync(0xffffffffu, upto - mine, l);
-  int t = l * per;
-  while (rank >= sm.tiles[t]) rank -= sm.tiles[t++];
-  return sample_scan(sp, mt, t * tv, min(sp.nvec, (t + 1) * tv), rank);
+  int id = sample_scan_few(sp, mt, 0, sp.head, rank);
+  if (id < 0) {
+    const int per = (nt + 31) / 32;
+    uint32_t sum = 0;
+    for (int i = lane * per; i < min(nt, (lane + 1) * per); ++i) sum += sm.tiles[i];
+    const uint32_t upto = warp_scan(sum);
+    const uint32_t hit = __ballot_sync(0xffffffffu, upto > rank);
+    if (hit == 0) {
+      rank -= __shfl_sync(0xffffffffu, upto, 31);
+      id = sample_scan_few(sp, mt, sp.tail_at, sp.tail, rank);
+    } else {
+      const int l = __ffs(hit) - 1;
+      rank -= __shfl_sync(0xffffffffu, upto - sum, l);
+      int t = l * per;
+      while (rank >= sm.tiles[t]) rank -= sm.tiles[t++];
+      id = sample_scan(sp, mt, t * tv, min(sp.nvec, (t + 1) * tv), rank);
+    }
+  }
+  if (lane == 0) *id_out = id;
 }
 
 __device__ __forceinline__ void sample_put(const SampleParams& p, int64_t row, int n, int id,
@@ -501,10 +750,45 @@ __device__ __forceinline__ void sample_bad(const SampleParams& p) {
   if (p.status) atomicOr(p.status, CKL_DEV_BAD_SAMPLE);
 }
 
+// Counts those of eight values that were drawn, in part `seg` of the row.  Most
+// were not: a bit for each bf16 pattern says so, which 32 lanes read with few
+// bank conflicts (32 neighbouring values share a word).
+__device__ __forceinline__ void sample_marked8(SampleShared& sm, const uint4& v, int seg) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t hits = 0;  // bit j: value j
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t lo = sm.drawn[(w[j] >> 5) & 0x7FFu], hi = sm.drawn[w[j] >> 21];
+    hits |= ((lo >> (w[j] & 31u)) & 1u) << (2 * j);
+    hits |= ((hi >> ((w[j] >> 16) & 31u)) & 1u) << (2 * j + 1);
+  }
+  while (hits) {
+    const int j = __ffs(hits) - 1;
+    hits &= hits - 1u;
+    const uint32_t word = j < 4 ? (j < 2 ? w[0] : w[1]) : (j < 6 ? w[2] : w[3]);
+    const uint32_t x = (j & 1) ? word >> 16 : word & 0xFFFFu;
+    const uint32_t col = sm.hist[sample_slot_of(x)] & (SM_BATCH - 1u);
+    atomicAdd(&sm.segs[seg][col >> 1], (col & 1u) ? 0x10000u : 1u);
+  }
+}
+
+__device__ __noinline__ void sample_marked_pass(SampleShared& sm, const uint4* __restrict__ z,
+                                                int nvec, int seg_vecs) {
+  int i = threadIdx.x;
+  for (; i + (SM_UNROLL - 1) * SM_THREADS < nvec; i += SM_UNROLL * SM_THREADS) {
+    uint4 v[SM_UNROLL];
+#pragma unroll
+    for (int k = 0; k < SM_UNROLL; ++k) v[k] = z[i + k * SM_THREADS];
+#pragma unroll
+    for (int k = 0; k < SM_UNROLL; ++k) sample_marked8(sm, v[k], (i + k * SM_THREADS) / seg_vecs);
+  }
+  for (; i < nvec; i += SM_THREADS) sample_marked8(sm, z[i], i / seg_vecs);
+}
+
 // A row whose finite values are not all covered: the key space in eight
 // windows, one pass over the row each, and a pass for every chunk looked into.
-__device__ __noinline__ void sample_row_any(SampleShared& sm, const SampleParams& p, int64_t row,
-                                            const SampleRow& r) {
+__device__ __noinline__ void sample_row_any(SampleShared& sm, const SampleParams& p, int64_t row) {
+  const SampleRow& r = sm.par;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint16_t* z = p.logits + row * p.ld;
   SampleKeys s{sm, z, p.V};
@@ -543,11 +827,10 @@ __device__ __noinline__ void sample_row_any(SampleShared& sm, const SampleParams
     }
   }
   __syncthreads();
-  if (warp == 0) sample_prefix(s.pc(), s.pw(), SM_ANY_CHUNKS);
-  __syncthreads();
+  sample_prefix(sm, s.pc(), s.pw(), SM_ANY_CHUNKS);
   double mass;
   const uint32_t L = sample_kept(s, m, r, mass);
-  const SampleSpan sp(z, p.V);
+  const SampleSpan sp(z, p.V, 1, 0);
   for (int n = 0; n < p.N; ++n) {
     const float u = p.u[row * p.N + n];
     if (!sample_u_ok(u)) {  // the same in all threads
@@ -571,7 +854,7 @@ __device__ __noinline__ void sample_row_any(SampleShared& sm, const SampleParams
           if (rank >= all) rank -= all;
           else id = sample_scan(sp, mt, v0, min(sp.nvec, v0 + 32), rank);
         }
-        if (id < 0) id = sample_scan_few(sp, mt, sp.tail_at(), sp.tail, rank);
+        if (id < 0) id = sample_scan_few(sp, mt, sp.tail_at, sp.tail, rank);
       }
       if (lane == 0) sample_put(p, row, n, id, static_cast<float>(log(d.w / mass)));
     }
@@ -581,52 +864,228 @@ __device__ __noinline__ void sample_row_any(SampleShared& sm, const SampleParams
 
 __device__ __forceinline__ SampleRow sample_row_params(const SampleParams& p, int64_t row) {
   SampleRow r;
-  r.temp = p.temperature_rows ? static_cast<double>(p.temperature_rows[row]) : p.temperature;
+  const double temp = p.temperature_rows ? static_cast<double>(p.temperature_rows[row]) : p.temperature;
   r.top_k = p.top_k_rows ? p.top_k_rows[row] : p.top_k;
   r.top_p = p.top_p_rows ? static_cast<double>(p.top_p_rows[row]) : p.top_p;
   r.min_p = p.min_p_rows ? static_cast<double>(p.min_p_rows[row]) : p.min_p;
-  r.ok = r.temp >= 0.0 && r.temp < INFINITY && r.top_p > 0.0 && r.min_p >= 0.0 && r.min_p <= 1.0;
-  r.greedy = r.temp == 0.0;
-  if (r.greedy) r.temp = 1.0;
+  r.ok = temp >= 0.0 && temp < INFINITY && r.top_p > 0.0 && r.min_p >= 0.0 && r.min_p <= 1.0;
+  r.greedy = temp == 0.0;
+  r.inv_temp = r.greedy ? 1.0 : 1.0 / temp;
   return r;
 }
 
-__global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const SampleParams p) {
+// Tokens and mass of the chunks a block of the row's C has (every C-th), to
+// all of them; four lanes a chunk.  The bins of a chunk are neighbours of one
+// binade, so their weights are a geometric series: two exponentials and a
+// product a bin.
+template <int C>
+__device__ __noinline__ void sample_chunks(SampleShared& sm, uint32_t rank, float m) {
+  const SampleRow r = sm.par;
+  static_assert(SM_CB == 16, "four lanes a chunk, four bins each");
+  constexpr int PER = SM_THREADS / 4;  // chunks of a pass
+  const int sub = threadIdx.x & 3;
+  for (int k0 = 0; k0 * C < SM_CHUNKS; k0 += PER) {  // whole warps: lanes add up below
+    const int c = rank + C * (k0 + static_cast<int>(threadIdx.x) / 4);
+    uint32_t n[4] = {0, 0, 0, 0};
+    // the lane's bins in slot order: ascending magnitudes
+    const int slot0 = c * SM_CB < SM_HALF ? SM_HALF - SM_CB - c * SM_CB : c * SM_CB;
+    const int slot = slot0 + 4 * sub;
+    if (c < SM_CHUNKS) {
+      uint4 v[C];
+#pragma unroll
+      for (int b = 0; b < C; ++b)
+        v[b] = C == 1 ? *reinterpret_cast<const uint4*>(&sm.hist[slot])
+                      : peer_load4(peer(&sm.hist[slot], b));
+#pragma unroll
+      for (int b = 0; b < C; ++b) {
+        n[0] += v[b].x;
+        n[1] += v[b].y;
+        n[2] += v[b].z;
+        n[3] += v[b].w;
+      }
+    }
+    uint32_t cnt = n[0] + n[1] + n[2] + n[3];
+    double w = 0.0;
+    if (cnt) {
+      const uint32_t b0 = slot < SM_HALF ? SM_LO + slot
+                                         : slot < SM_NEG ? 0u : 0x8000u + SM_LO + (slot - SM_NEG);
+      const float v0 = bf16_value(b0), v3 = bf16_value(b0 + 3);
+      const double gap = (static_cast<double>(bf16_value(b0 + 1)) - v0) * r.inv_temp;
+      // bin by bin where the largest logit is (its weight is 1 exactly), and at
+      // low temperatures (the series would leave fp64's range)
+      if (fabs(gap) < 20.0 && (m < fminf(v0, v3) || m > fmaxf(v0, v3))) {
+        const double e = sample_weight(bf16_value(b0), m, r), ratio = exp(gap);
+        w = e * (n[0] + ratio * (n[1] + ratio * (n[2] + ratio * n[3])));
+      } else {
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t nk = k < 2 ? (k ? n[1] : n[0]) : (k == 2 ? n[2] : n[3]);
+          if (nk) w += nk * sample_weight(bf16_value(b0 + k), m, r);
+        }
+      }
+    }
+    cnt += __shfl_xor_sync(0xffffffffu, cnt, 1);
+    cnt += __shfl_xor_sync(0xffffffffu, cnt, 2);
+    w += __shfl_xor_sync(0xffffffffu, w, 1);
+    w += __shfl_xor_sync(0xffffffffu, w, 2);
+    if (c >= SM_CHUNKS) continue;
+    if constexpr (C == 1) {
+      if (sub == 0) {
+        sm.pc[c] = cnt;
+        sm.pw[c] = w;
+      }
+    } else {
+      for (int b = sub; b < C; b += 4) {
+        peer_store(peer(&sm.pc[c], b), cnt);
+        peer_store(peer(&sm.pw[c], b), w);
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void sample_no_draw(const SampleParams& p, int64_t row, int n) {
+  sample_put(p, row, n, -1, __int_as_float(0x7FC00000));
+}
+
+// Up to 64 draws of a row: the counters of the drawn values become marks, one
+// pass counts each marked value in every part of the row, and each draw reads
+// the one part that holds its occurrence.
+template <int C>
+__device__ __noinline__ void sample_batch(SampleShared& sm, const SampleParams& p, int64_t row,
+                                          const SampleSpan sp, uint32_t rank, float m, int n0) {
+  const SampleRow& r = sm.par;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const SampleBins<C> s{sm};
+  const uint32_t L = sm.kept;
+  const double mass = sm.mass;
+  const int nb = min(SM_BATCH, p.N - n0);
+  const int seg_vecs = max(32, ((sp.nvec + SM_SEGS - 1) / SM_SEGS + 31) / 32 * 32);
+  if (tid < nb) {  // a draw a thread
+    const float u = p.u[row * p.N + n0 + tid];
+    const bool ok = sample_u_ok(u);
+    const SamplePlace d = sample_draw_lane(s, m, r, L, mass, ok ? u : 0.f);
+    sm.draw_bin[tid] = ok ? d.bin : 0xFFFFFFFFu;
+    sm.draw_rank[tid] = d.in_bin;
+    if (rank == 0) {
+      if (!ok) {
+        sample_no_draw(p, row, n0 + tid);
+        sample_bad(p);
+      } else if (p.logp) {
+        p.logp[row * p.N + n0 + tid] = static_cast<float>(log(d.w / mass));
+      }
+    }
+  }
+  for (int i = tid; i < SM_SEGS * SM_BATCH / 2; i += SM_THREADS) (&sm.segs[0][0])[i] = 0;
+  for (int i = tid; i < 65536 / 32; i += SM_THREADS) sm.drawn[i] = 0;
+  sync_all<C>();  // no block reads another's counters any more
+  // mark: 0x80000000 | the draw whose column counts the value; the count
+  // itself is kept by the draw's thread and put back behind the pass
+  uint32_t* at = nullptr;
+  uint32_t kept = 0;
+  if (tid < nb && sm.draw_bin[tid] != 0xFFFFFFFFu) {
+    const int bin = static_cast<int>(sm.draw_bin[tid]);
+    at = &sm.hist[sample_bin_slot(bin)];
+    kept = *at;
+    const uint32_t x = sample_bin_bits(bin);
+    atomicOr(&sm.drawn[x / 32], 1u << (x % 32));
+    if (x == 0u) atomicOr(&sm.drawn[0x8000 / 32], 1u);  // -0
+  }
+  __syncthreads();
+  if (at) atomicMax(at, 0x80000000u | static_cast<uint32_t>(tid));
+  __syncthreads();
+  sample_marked_pass(sm, sp.v, sp.nvec, seg_vecs);
+  __syncthreads();
+  auto in_part = [&](uint32_t seg, uint32_t col) {
+    return (sm.segs[seg][col >> 1] >> ((col & 1u) * 16u)) & 0xFFFFu;
+  };
+  if constexpr (C > 1) {  // how often this block has each drawn value
+    for (int n = warp; n < nb; n += SM_WARPS) {
+      const uint32_t bin = sm.draw_bin[n];
+      if (bin == 0xFFFFFFFFu) continue;
+      const uint32_t col = sm.hist[sample_bin_slot(static_cast<int>(bin))] & (SM_BATCH - 1u);
+      const SampleMatch mt(sample_bin_bits(static_cast<int>(bin)));
+      const bool few = lane < sp.head ? mt.is(sp.z[lane])
+                                      : lane < sp.head + sp.tail &&
+                                            mt.is(sp.z[sp.tail_at + lane - sp.head]);
+      const uint32_t all =
+          __reduce_add_sync(0xffffffffu, in_part(lane, col) + in_part(lane + 32, col) +
+                                             in_part(lane + 64, col) + in_part(lane + 96, col)) +
+          __popc(__ballot_sync(0xffffffffu, few));
+      if (lane < C) peer_store(peer(&sm.found[rank][n], lane), all);
+    }
+    sync_all<C>();
+  }
+  for (int n = warp; n < nb; n += SM_WARPS) {
+    const uint32_t bin = sm.draw_bin[n];
+    if (bin == 0xFFFFFFFFu) continue;
+    const uint32_t col = sm.hist[sample_bin_slot(static_cast<int>(bin))] & (SM_BATCH - 1u);
+    const SampleMatch mt(sample_bin_bits(static_cast<int>(bin)));
+    uint32_t left = sm.draw_rank[n];
+    if constexpr (C > 1) {
+      bool here = true;
+      for (uint32_t k = 0; k < rank && here; ++k) {
+        if (left < sm.found[k][n]) here = false;  // in a block before this one
+        else left -= sm.found[k][n];
+      }
+      if (!here || left >= sm.found[rank][n]) continue;
+    }
+    int id = sample_scan_few(sp, mt, 0, sp.head, left);
+    if (id < 0) {
+      // lane l: parts 4 l .. 4 l + 3
+      uint32_t c[4], sum = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        c[k] = in_part(4 * lane + k, col);
+        sum += c[k];
+      }
+      const uint32_t upto = warp_scan(sum);
+      const uint32_t hit = __ballot_sync(0xffffffffu, upto > left);
+      if (hit == 0) {
+        left -= __shfl_sync(0xffffffffu, upto, 31);
+        id = sample_scan_few(sp, mt, sp.tail_at, sp.tail, left);
+      } else {
+        const int l = __ffs(hit) - 1;
+        uint32_t in = left - (upto - sum);
+        int seg = 4 * lane;
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          if (seg == 4 * lane + k && in >= c[k]) {
+            in -= c[k];
+            ++seg;
+          }
+        in = __shfl_sync(0xffffffffu, in, l);
+        seg = __shfl_sync(0xffffffffu, seg, l);
+        id = sample_scan(sp, mt, seg * seg_vecs, min(sp.nvec, (seg + 1) * seg_vecs), in);
+      }
+    }
+    if (lane == 0) p.ids[row * p.N + n0 + n] = id;
+  }
+  __syncthreads();
+  if (at) *at = kept;
+  sync_all<C>();  // the counters are as they were, for the next draws
+}
+
+template <int C>
+__global__ void __launch_bounds__(SM_THREADS, SM_BLOCKS) sample_kernel(const __grid_constant__ SampleParams p) {
   extern __shared__ __align__(16) uint8_t sample_smem[];
   SampleShared& sm = *reinterpret_cast<SampleShared*>(sample_smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
-    const SampleSpan sp(p.logits + row * p.ld, p.V);
-    const SampleRow r = sample_row_params(p, row);
-    __syncthreads();  // the last row's reads of shared memory
-    for (int i = tid; i < SM_SLOTS / 4; i += SM_THREADS)
+  const uint32_t rank = C == 1 ? 0u : cluster_ctarank();
+  for (int64_t row = blockIdx.x / C; row < p.T; row += gridDim.x / C) {
+    const SampleSpan sp(p.logits + row * p.ld, p.V, C, rank);
+    sync_all<C>();  // the last row's reads of shared memory
+    if (tid == 0) sm.par = sample_row_params(p, row);
+    for (int i = tid; i < SM_BINS / 4; i += SM_THREADS)
       reinterpret_cast<uint4*>(sm.hist)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
 
     // ---- how often each value occurs, and the largest
-    uint32_t flags = 0;
-    uint32_t m2 = 0xFF80FF80u;
-    for (int i = tid; i < sp.nvec; i += SM_THREADS) {
-      const uint4 v = sp.v[i];
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      m2 = bf16x2_max(m2, bf16x2_max(bf16x2_max(v.x, v.y), bf16x2_max(v.z, v.w)));
-      if ((sample_outside(v.x) | sample_outside(v.y) | sample_outside(v.z) |
-           sample_outside(v.w)) == 0u) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          atomicAdd(&sm.hist[sample_slot(w[j] & 0xFFFFu)], 1u);
-          atomicAdd(&sm.hist[sample_slot(w[j] >> 16)], 1u);
-        }
-      } else {
-        for (int j = 0; j < 4; ++j) {
-          sample_count1(sm.hist, w[j] & 0xFFFFu, flags);
-          sample_count1(sm.hist, w[j] >> 16, flags);
-        }
-      }
-    }
+    const uint64_t seen = sample_count_pass(sm.hist, sp.v, sp.nvec);
+    const uint32_t m2 = static_cast<uint32_t>(seen);
+    uint32_t flags = static_cast<uint32_t>(seen >> 32);
     float m = fmaxf(bf16_lo(m2), bf16_hi(m2));
     if (tid < sp.head + sp.tail) {
-      const uint32_t x = sp.z[tid < sp.head ? tid : sp.tail_at() + tid - sp.head];
+      const uint32_t x = sp.z[tid < sp.head ? tid : sp.tail_at + tid - sp.head];
       sample_count1(sm.hist, x, flags);
       m = fmaxf(m, bf16_value(x));
     }
@@ -642,152 +1101,83 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const SampleParam
       m = fmaxf(m, sm.red[w]);
       flags |= sm.flags[w];
     }
+    if constexpr (C > 1) {
+      if (tid == 0) {
+        sm.row_max = m;
+        sm.row_flags = flags;
+      }
+      sync_all<C>();
+#pragma unroll
+      for (int b = 0; b < C; ++b) {
+        m = fmaxf(m, __uint_as_float(peer_load(peer(&sm.row_max, b))));
+        flags |= peer_load(peer(&sm.row_flags, b));
+      }
+    }
     if (m == 0.f) m = 0.f;  // -0 counts as +0
 
+    // the rest is decided alike in all blocks of the row
+    const SampleRow& r = sm.par;
     const bool bad = !r.ok || (flags & SF_BAD);
     if (bad || m == -INFINITY) {  // no answer: bad numbers, or nothing left to draw
-      for (int n = tid; n < p.N; n += SM_THREADS)
-        sample_put(p, row, n, -1, __int_as_float(0x7FC00000));
-      if (bad && tid == 0) sample_bad(p);
+      if (rank == 0)
+        for (int n = tid; n < p.N; n += SM_THREADS) sample_no_draw(p, row, n);
+      if (bad && rank == 0 && tid == 0) sample_bad(p);
       continue;
     }
     // values of -256 and less weigh at most 2^((-256 - m) log2(e) / temp)
     const bool low_counts =
         (flags & SF_LOW) &&
-        (m <= -256.f || (!r.greedy && (m + 256.0) * 1.4426950408889634 < 64.0 * r.temp));
+        (m <= -256.f || (!r.greedy && (m + 256.0) * 1.4426950408889634 * r.inv_temp < 64.0));
     if ((flags & SF_ANY) || low_counts) {
-      sample_row_any(sm, p, row, r);
+      if (rank == 0) sample_row_any(sm, p, row);
       continue;
     }
 
-    // ---- tokens and mass of every chunk of 32 values, then before each
-    const SampleBins s{sm};
-    for (int c = warp; c < SM_CHUNKS; c += SM_WARPS) {
-      const uint32_t n = s.count(c);
-      uint32_t cnt = 0;
-      double w = 0.0;
-      if (__any_sync(0xffffffffu, n != 0)) {
-        if (n) w = n * sample_weight(s.value(c * 32 + lane), m, r);
-        w = warp_sum(w);
-        cnt = __reduce_add_sync(0xffffffffu, n);
+    // ---- tokens and mass before every chunk of values
+    sample_chunks<C>(sm, rank, m);
+    sync_all<C>();
+    sample_prefix(sm, sm.pc, sm.pw, SM_CHUNKS);
+
+    // ---- what the filters keep, the draws
+    if (warp == 0) {
+      const SampleBins<C> s{sm};
+      double mass;
+      const uint32_t L = sample_kept(s, m, r, mass);
+      if (p.N == 1) {
+        const float u = p.u[row];
+        const bool ok = sample_u_ok(u);
+        const SamplePlace d = sample_draw(s, m, r, L, mass, ok ? u : 0.f);
+        if (lane == 0) {
+          sm.draw_bin[0] = ok ? d.bin : 0xFFFFFFFFu;
+          sm.draw_rank[0] = d.in_bin;
+          sm.draw_w = d.w;
+        }
       }
       if (lane == 0) {
-        sm.pc[c] = cnt;
-        sm.pw[c] = w;
+        sm.kept = L;
+        sm.mass = mass;
       }
     }
     __syncthreads();
-    if (warp == 0) sample_prefix(sm.pc, sm.pw, SM_CHUNKS);
-    __syncthreads();
-
-    // ---- what the filters keep (every warp for itself), the draws
-    double mass;
-    const uint32_t L = sample_kept(s, m, r, mass);
     if (p.N == 1) {
-      const float u = p.u[row];
-      if (!sample_u_ok(u)) {
-        if (tid == 0) {
-          sample_put(p, row, 0, -1, __int_as_float(0x7FC00000));
+      const uint32_t bin = sm.draw_bin[0];
+      if (bin == 0xFFFFFFFFu) {
+        if (rank == 0 && tid == 0) {
+          sample_no_draw(p, row, 0);
           sample_bad(p);
         }
         continue;
       }
-      const SamplePlace d = sample_draw(s, m, r, L, mass, u);
-      const int id = sample_find(sm, sp, sample_bin_bits(d.bin), d.in_bin);
-      if (tid == 0) sample_put(p, row, 0, id, static_cast<float>(log(d.w / mass)));
+      if (rank == 0 && tid == 32 && p.logp)
+        p.logp[row] = static_cast<float>(log(sm.draw_w / sm.mass));
+      sample_find<C>(sm, sp, rank, sample_bin_bits(static_cast<int>(bin)), sm.draw_rank[0],
+                     p.ids + row);
       continue;
     }
-
-    // ---- many draws: the counters of the drawn values become marks, and one
-    // pass counts each marked value in every part of the row
-    const int seg_vecs = max(32, ((sp.nvec + SM_SEGS - 1) / SM_SEGS + 31) / 32 * 32);
-    for (int n0 = 0; n0 < p.N; n0 += SM_BATCH) {
-      const int nb = min(SM_BATCH, p.N - n0);
-      __syncthreads();
-      for (int n = warp; n < nb; n += SM_WARPS) {
-        const float u = p.u[row * p.N + n0 + n];
-        const bool ok = sample_u_ok(u);
-        const SamplePlace d = sample_draw(s, m, r, L, mass, ok ? u : 0.f);
-        if (lane == 0) {
-          sm.draw_bin[n] = ok ? d.bin : 0xFFFFFFFFu;
-          sm.draw_rank[n] = d.in_bin;
-          if (!ok) {
-            sample_put(p, row, n0 + n, -1, __int_as_float(0x7FC00000));
-            sample_bad(p);
-          } else if (p.logp) {
-            p.logp[row * p.N + n0 + n] = static_cast<float>(log(d.w / mass));
-          }
-        }
-      }
-      for (int i = tid; i < SM_SEGS * SM_BATCH / 2; i += SM_THREADS) (&sm.segs[0][0])[i] = 0;
-      __syncthreads();
-      // mark: 0x80000000 | the draw whose column counts the value; the count
-      // itself is kept by the draw's thread and put back behind the pass
-      uint32_t* at = nullptr;
-      uint32_t kept = 0;
-      if (tid < nb && sm.draw_bin[tid] != 0xFFFFFFFFu) {
-        at = &sm.hist[sample_bin_slot(static_cast<int>(sm.draw_bin[tid]))];
-        kept = *at;
-      }
-      __syncthreads();
-      if (at) atomicMax(at, 0x80000000u | static_cast<uint32_t>(tid));
-      __syncthreads();
-      auto count = [&](uint32_t x, int seg) {
-        const uint32_t a = x & 0x7FFFu;
-        if (a != 0u && (a < SM_LO || a >= SM_HI)) return;
-        const uint32_t h = sm.hist[sample_slot_of(x)];
-        if (h & 0x80000000u)
-          atomicAdd(&sm.segs[seg][(h & 63u) >> 1], (h & 1u) ? 0x10000u : 1u);
-      };
-      for (int i = tid; i < sp.nvec; i += SM_THREADS) {
-        const uint4 v = sp.v[i];
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        const int seg = i / seg_vecs;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          count(w[j] & 0xFFFFu, seg);
-          count(w[j] >> 16, seg);
-        }
-      }
-      __syncthreads();
-      for (int n = warp; n < nb; n += SM_WARPS) {
-        const uint32_t bin = sm.draw_bin[n];
-        if (bin == 0xFFFFFFFFu) continue;
-        const uint32_t col = sm.hist[sample_bin_slot(static_cast<int>(bin))] & 63u;
-        const SampleMatch mt(sample_bin_bits(static_cast<int>(bin)));
-        uint32_t rank = sm.draw_rank[n];
-        int id = sample_scan_few(sp, mt, 0, sp.head, rank);
-        if (id < 0) {
-          // lane l: parts 4 l .. 4 l + 3
-          uint32_t c[4], sum = 0;
-          for (int k = 0; k < 4; ++k) {
-            c[k] = (sm.segs[4 * lane + k][col >> 1] >> ((col & 1u) * 16u)) & 0xFFFFu;
-            sum += c[k];
-          }
-          const uint32_t upto = warp_scan(sum);
-          const uint32_t hit = __ballot_sync(0xffffffffu, upto > rank);
-          if (hit == 0) {
-            rank -= __shfl_sync(0xffffffffu, upto, 31);
-            id = sample_scan_few(sp, mt, sp.tail_at(), sp.tail, rank);
-          } else {
-            const int l = __ffs(hit) - 1;
-            uint32_t left = rank - (upto - sum);
-            int seg = 4 * lane;
-            for (int k = 0; k < 3 && left >= c[k]; ++k) {
-              left -= c[k];
-              ++seg;
-            }
-            left = __shfl_sync(0xffffffffu, left, l);
-            seg = __shfl_sync(0xffffffffu, seg, l);
-            id = sample_scan(sp, mt, seg * seg_vecs, min(sp.nvec, (seg + 1) * seg_vecs), left);
-          }
-        }
-        if (lane == 0) p.ids[row * p.N + n0 + n] = id;
-      }
-      __syncthreads();
-      if (at) *at = kept;
-    }
+    for (int n0 = 0; n0 < p.N; n0 += SM_BATCH)
+      sample_batch<C>(sm, p, row, sp, rank, m, n0);
   }
+  if constexpr (C > 1) sync_all<C>();  // no block leaves while another reads its counters
 }
 
 }  // namespace ckl

@@ -28,7 +28,7 @@ enum {
 /* Elements of a row that share a scale in the 8-bit form. */
 #define CKL_ACT8_GROUP 32
 /* Largest vocabulary of ckl_sample. */
-#define CKL_SAMPLE_MAX_V 4194304
+#define CKL_SAMPLE_MAX_V 2097152
 /* Bit of ckl_sample's device_status: a NaN or +inf logit, or a row's parameter
  * or number out of range. */
 #define CKL_SAMPLE_BAD_INPUT 16

@@ -108,7 +108,7 @@ def test_sample_refusals(ckl):
         assert s(_8=bad) == 1
     for bad in (-0.1, 1.5, float("nan")):
         assert s(_9=bad) == 1
-    assert s(_1=1 << 23, _3=(1 << 22) + 1) == 2
+    assert s(_1=1 << 23, _3=(1 << 21) + 1) == 2
 
 
 def test_binding_refuses_cpu_tensors(ckl):
