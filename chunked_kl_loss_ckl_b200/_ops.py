@@ -5,11 +5,12 @@ offers every name of ``__all__`` as its own."""
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import CKL_OK, LIB_PATH, CklError, _ptr, backward, forward, lib
+from . import CKL_OK, LIB_PATH, CklError, backward, forward, lib
 
 __all__ = [
     "ACT8_GROUP", "SAMPLE_BAD_INPUT", "act8_pack", "act8_unpack", "norm_forward",
@@ -46,19 +47,28 @@ def _bind(L):
 _bind(lib)
 
 
+# The raw handle of a device's current stream: building a torch.cuda.Stream
+# for it takes longer than launching a small kernel.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _on(t, stream, call):
     """call(stream handle) with t's device current and, when one is given,
     ``stream`` current too, so that what the call allocates belongs to it."""
-    dev = t.device
-    if stream is None and dev.index == torch.cuda.current_device():
-        return call(torch.cuda.current_stream().cuda_stream)
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
+    dev = t.get_device()
+    if stream is None and dev == torch.cuda.current_device():
+        return call(_raw_stream(dev))
+    if stream is not None and stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {t.device}")
     with torch.cuda.device(dev):
         if stream is None:
-            return call(torch.cuda.current_stream().cuda_stream)
+            return call(_raw_stream(dev))
         with torch.cuda.stream(stream):
             return call(stream.cuda_stream)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _check(name, t, dtypes, shape=None, like=None):
@@ -68,9 +78,9 @@ def _check(name, t, dtypes, shape=None, like=None):
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if like is not None and t.device != like.device:
+    if like is not None and t.get_device() != like.get_device():
         raise ValueError(f"{name} is on {t.device}, expected {like.device}")
 
 
@@ -96,8 +106,8 @@ def act8_pack(x, stream=None):
     qs, es = _kept_shapes(x.shape)
 
     def call(st):
-        q = torch.empty(qs, dtype=torch.int8, device=x.device)
-        e = torch.empty(es, dtype=torch.uint8, device=x.device)
+        q = x.new_empty(qs, dtype=torch.int8)
+        e = x.new_empty(es, dtype=torch.uint8)
         rc = lib.ckl_act8_pack(_ptr(x), _DTYPES[x.dtype], T, d, _ptr(q), _ptr(e), st)
         if rc != CKL_OK:
             raise CklError(rc, "ckl_act8_pack")
@@ -120,7 +130,7 @@ def act8_unpack(q, exponents, dtype=torch.bfloat16, stream=None):
         raise TypeError(f"dtype must be one of {tuple(_DTYPES)}")
 
     def call(st):
-        x = torch.empty(q.shape, dtype=dtype, device=q.device)
+        x = torch.empty_like(q, dtype=dtype)
         rc = lib.ckl_act8_unpack(_ptr(q), _ptr(exponents), T, d, _DTYPES[dtype], _ptr(x), st)
         if rc != CKL_OK:
             raise CklError(rc, "ckl_act8_unpack")
@@ -157,15 +167,14 @@ def norm_forward(x, gamma=None, beta=None, eps: float = 1e-5, center: bool = Tru
         _check("out", out, (x.dtype,), x.shape, like=x)
 
     def call(st):
-        dev = x.device
         y = out if out is not None else torch.empty_like(x)
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+        rstd = x.new_empty(x.shape[:-1], dtype=torch.float32)
         mean = torch.empty_like(rstd) if center else None
         q = e = kept = None
         if checkpoint:
             qs, es = _kept_shapes(x.shape)
-            q = torch.empty(qs, dtype=torch.int8, device=dev)
-            e = torch.empty(es, dtype=torch.uint8, device=dev)
+            q = x.new_empty(qs, dtype=torch.int8)
+            e = x.new_empty(es, dtype=torch.uint8)
             kept = (q, e)
         rc = lib.ckl_norm_forward(_ptr(x), _DTYPES[x.dtype], _ptr(gamma), _ptr(beta), pd, T, d,
                                   eps, _ptr(y), _ptr(mean), _ptr(rstd), _ptr(q), _ptr(e), st)
@@ -176,6 +185,7 @@ def norm_forward(x, gamma=None, beta=None, eps: float = 1e-5, center: bool = Tru
     return _on(x, stream, call)
 
 
+@functools.lru_cache(maxsize=1024)
 def norm_workspace_bytes(T: int, d: int) -> int:
     n = lib.ckl_norm_workspace_bytes(T, d)
     if n == 0:
@@ -225,14 +235,14 @@ def norm_backward(dy, x, mean, rstd, gamma=None, bias: bool = False, dgamma=None
         dx = out_dx if out_dx is not None else torch.empty_like(dy)
         dg = dgamma
         if dg is None and gamma is not None:
-            dg = torch.empty(d, dtype=torch.float32, device=dy.device)
+            dg = rstd.new_empty(d)
         db = dbeta
         if db is None and bias:
-            db = torch.empty(d, dtype=torch.float32, device=dy.device)
+            db = rstd.new_empty(d)
         ws, n = workspace, 0
         if dg is not None or db is not None:
             if ws is None:
-                ws = torch.empty(norm_workspace_bytes(T, d), dtype=torch.uint8, device=dy.device)
+                ws = dy.new_empty(norm_workspace_bytes(T, d), dtype=torch.uint8)
             n = ws.numel()
         rc = lib.ckl_norm_backward(_ptr(dy), _DTYPES[dy.dtype], _ptr(x), _ptr(q), _ptr(e),
                                    _ptr(mean), _ptr(rstd), _ptr(gamma), pd, T, d, _ptr(dx),
@@ -354,8 +364,8 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, stream=Non
         _check("status", status, (torch.int32,), (1,), like=logits)
 
     def call(st):
-        ids = torch.empty(u.shape, dtype=torch.int32, device=u.device)
-        logp = torch.empty(u.shape, dtype=torch.float32, device=u.device)
+        ids = torch.empty_like(u, dtype=torch.int32)
+        logp = torch.empty_like(u)
         rc = lib.ckl_sample(_ptr(logits), ld, T, V, _ptr(u), N, *numbers, *rows, _ptr(ids),
                             _ptr(logp), _ptr(status), st)
         if rc != CKL_OK:

@@ -218,13 +218,11 @@ int norm_bwd_launch(const ckl::NormBwd& p0, bool vec, int sms, cudaStream_t st, 
       dim3(rows), ckl::NORM_THREADS, 0, st);
 }
 
-#ifndef CKL_SAMPLE_PLACES
-#define CKL_SAMPLE_PLACES 2
-#endif
-template <int C>
+template <int C, bool MANY>
 int sample_launch(const ckl::SampleParams& p, int sms, cudaStream_t st) {
-  const size_t smem = sizeof(ckl::SampleShared);
-  if (cudaFuncSetAttribute(ckl::sample_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  auto* k = ckl::sample_kernel<C, MANY>;
+  const size_t smem = MANY ? sizeof(ckl::SampleShared) : ckl::SM_ONE_BYTES;
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(smem)) != cudaSuccess)
     return CKL_ERR_CUDA;
   cudaLaunchAttribute cluster;
@@ -233,15 +231,25 @@ int sample_launch(const ckl::SampleParams& p, int sms, cudaStream_t st) {
   cluster.val.clusterDim.y = 1;
   cluster.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(
-      std::min<int64_t>(p.T, std::max(1, sms * ckl::SM_BLOCKS / C)) * C));
-  cfg.blockDim = dim3(ckl::SM_THREADS);
+  const int64_t rows = std::max(1, sms * ckl::sample_blocks(MANY) / C);  // at a time
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min(p.T, rows) * C));
+  cfg.blockDim = dim3(ckl::sample_threads(MANY));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = &cluster;
   cfg.numAttrs = C > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, ckl::sample_kernel<C>, p) == cudaSuccess ? CKL_OK
-                                                                         : CKL_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, k, p) == cudaSuccess ? CKL_OK : CKL_ERR_CUDA;
+}
+
+// Blocks a row: as many as two blocks an SM hold at a time (of 512 threads not
+// quite: clusters have to fit into groups of SMs, 74 of four do not, 64 do).
+template <bool MANY>
+int sample_rows(const ckl::SampleParams& p, int sms, cudaStream_t st) {
+  const int64_t places = MANY ? static_cast<int64_t>(sms) * 7 / 4 : static_cast<int64_t>(sms) * 2;
+  if (p.T * 8 <= places) return sample_launch<8, MANY>(p, sms, st);
+  if (p.T * 4 <= places) return sample_launch<4, MANY>(p, sms, st);
+  if (p.T * 2 <= places) return sample_launch<2, MANY>(p, sms, st);
+  return sample_launch<1, MANY>(p, sms, st);
 }
 
 bool norm_sizes_ok(int64_t T, int64_t d) {
@@ -429,13 +437,8 @@ int ckl_sample(const uint16_t* logits, int64_t ld, int64_t T, int64_t V, const f
   p.ids = ids;
   p.logp = logp;
   p.status = device_status;
-  // blocks a row: as many as keep all SMs' places filled
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int64_t places = static_cast<int64_t>(dev.sms) * CKL_SAMPLE_PLACES;
-  if (T * 8 <= places) return sample_launch<8>(p, dev.sms, st);
-  if (T * 4 <= places) return sample_launch<4>(p, dev.sms, st);
-  if (T * 2 <= places) return sample_launch<2>(p, dev.sms, st);
-  return sample_launch<1>(p, dev.sms, st);
+  return N == 1 ? sample_rows<false>(p, dev.sms, st) : sample_rows<true>(p, dev.sms, st);
 }
 
 }  // extern "C"

@@ -30,6 +30,7 @@
 // and each look for the drawn value in their own part.
 #pragma once
 
+#include <cstddef>
 #include <cstdint>
 
 #include "ckl_bf16.cuh"
@@ -39,16 +40,13 @@
 
 namespace ckl {
 
-#ifndef CKL_SM_THREADS
-#define CKL_SM_THREADS 512
-#endif
-#ifndef CKL_SM_BLOCKS
-#define CKL_SM_BLOCKS 2
-#endif
-constexpr int SM_THREADS = CKL_SM_THREADS;
-constexpr int SM_BLOCKS = CKL_SM_BLOCKS;        // of an SM, by their shared memory
-constexpr int SM_WARPS = SM_THREADS / 32;
+// Threads of a block and blocks of an SM: by shared memory three blocks fit
+// that draw once a row, two that draw many times.
+__host__ __device__ constexpr int sample_threads(bool many) { return many ? 512 : 256; }
+__host__ __device__ constexpr int sample_blocks(bool many) { return many ? 2 : 3; }
+constexpr int SM_MAX_WARPS = 16;
 constexpr int SM_UNROLL = 4;                    // 16-byte loads a thread has under way
+constexpr int SM_TILE_UNROLL = 8;               // the same, where little is done to them
 constexpr int SM_MAX_CLUSTER = 8;
 constexpr uint32_t SM_LO = 0x2B80;              // bf16 bits of 2^-40
 constexpr uint32_t SM_HI = 0x4380;              // bf16 bits of 256
@@ -62,10 +60,9 @@ static_assert(SM_HALF % 128 == 0 && SM_LO % 128 == 0 && 128 % SM_CB == 0,
 constexpr int SM_WIN = 8192;                    // keys of a window (rows of any values)
 constexpr int SM_ANY_CB = 32;
 constexpr int SM_ANY_CHUNKS = 65536 / SM_ANY_CB;
-constexpr int SM_TILES = 1024;                  // tiles whose matches are counted, at most
 constexpr int SM_SEGS = 128;                    // parts of the row counted per draw
 constexpr int SM_BATCH = 64;                    // draws found in one pass
-static_assert(SM_BATCH <= SM_THREADS, "a draw a thread");
+static_assert(SM_BATCH <= sample_threads(true), "a draw a thread");
 
 struct SampleParams {
   const uint16_t* logits;
@@ -96,28 +93,35 @@ struct alignas(16) SampleShared {
   // window's 8192 counters, the prefix masses of all 2048 chunks
   uint32_t hist[SM_BINS];
   double pw[SM_CHUNKS + 1];    // mass before each chunk
-  double scan_w[SM_WARPS];
+  double scan_w[SM_MAX_WARPS];
   double mass;                 // what the filters keep
   double draw_w;               // of the one draw
+  SampleRow par;
   uint32_t pc[SM_CHUNKS + 1];  // tokens before each chunk
-  uint32_t scan_c[SM_WARPS];
+  uint32_t scan_c[SM_MAX_WARPS];
   uint32_t kept;
-  union {
-    uint16_t tiles[SM_TILES];               // matches of one value in each tile
-    uint32_t segs[SM_SEGS][SM_BATCH / 2];   // matches of up to 64 values in each part, 16 bits each
-    uint32_t any_pc[SM_ANY_CHUNKS + 1];
-  };
-  uint32_t draw_bin[SM_BATCH], draw_rank[SM_BATCH];
-  uint32_t drawn[65536 / 32];  // a bit for each bf16 pattern that was drawn
-  uint32_t found[SM_MAX_CLUSTER][SM_BATCH];  // matches of the drawn values in each block's part
   uint32_t cb[SM_ANY_CB];  // one chunk's counters (rows of any values)
-  float red[SM_WARPS];
-  uint32_t flags[SM_WARPS];
+  float red[SM_MAX_WARPS];
+  uint32_t flags[SM_MAX_WARPS];
   float row_max;  // of this block's part
   uint32_t row_flags;
-  SampleRow par;
+  uint32_t draw_bin[SM_BATCH], draw_rank[SM_BATCH];
+  uint32_t found[SM_MAX_CLUSTER][SM_BATCH];  // matches of the drawn values in each block's part
+  union {
+    uint32_t any_pc[SM_ANY_CHUNKS + 1];
+    struct {                   // many draws; not there in launches for one
+      uint32_t segs[SM_SEGS][SM_BATCH / 2];  // matches of 64 values in each part, 16 bits each
+      uint32_t drawn[65536 / 32];            // a bit for each bf16 pattern that was drawn
+    };
+  };
 };
+// Bytes of a launch for one draw a row.
+constexpr size_t SM_ONE_BYTES =
+    offsetof(SampleShared, any_pc) + sizeof(uint32_t) * (SM_ANY_CHUNKS + 1);
 static_assert(SM_WIN * 4 + (SM_ANY_CHUNKS + 1) * 8 <= SM_BINS * 4, "prefix masses behind a window");
+
+__device__ __forceinline__ int sample_nt() { return static_cast<int>(blockDim.x); }
+__device__ __forceinline__ int sample_nw() { return static_cast<int>(blockDim.x) / 32; }
 
 enum : uint32_t { SF_BAD = 1, SF_LOW = 2, SF_ANY = 4 };
 
@@ -186,22 +190,36 @@ __device__ __forceinline__ void sample_count1(uint32_t* hist, uint32_t x, uint32
   }
 }
 
-// Counts eight values, and keeps the largest of those seen.
+// Counts eight values, and keeps the largest of those seen.  Values outside
+// the covered range are skipped; unless they are -inf (a mask's), they are
+// looked at one by one.
 __device__ __forceinline__ void sample_count8(uint32_t* hist, const uint4& v, uint32_t& m2,
                                               uint32_t& flags) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const uint32_t out[4] = {sample_outside(v.x), sample_outside(v.y), sample_outside(v.z),
+                           sample_outside(v.w)};
   m2 = bf16x2_max(m2, bf16x2_max(bf16x2_max(v.x, v.y), bf16x2_max(v.z, v.w)));
-  if ((sample_outside(v.x) | sample_outside(v.y) | sample_outside(v.z) | sample_outside(v.w)) ==
-      0u) {
+  if ((out[0] | out[1] | out[2] | out[3]) == 0u) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       atomicAdd(&hist[sample_slot(w[j] & 0xFFFFu)], 1u);
       atomicAdd(&hist[sample_slot(w[j] >> 16)], 1u);
     }
-  } else {
+    return;
+  }
+  uint32_t others = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (!(out[j] & 0x8000u)) atomicAdd(&hist[sample_slot(w[j] & 0xFFFFu)], 1u);
+    if (!(out[j] & 0x80000000u)) atomicAdd(&hist[sample_slot(w[j] >> 16)], 1u);
+    // the halves that are outside and not -inf
+    const uint32_t d = w[j] ^ 0xFF80FF80u;
+    others |= out[j] & (((d & 0x7FFF7FFFu) + 0x7FFF7FFFu) | d);
+  }
+  if (others) {
     for (int j = 0; j < 4; ++j) {
-      sample_count1(hist, w[j] & 0xFFFFu, flags);
-      sample_count1(hist, w[j] >> 16, flags);
+      if (out[j] & 0x8000u) sample_count1(hist, w[j] & 0xFFFFu, flags);
+      if (out[j] & 0x80000000u) sample_count1(hist, w[j] >> 16, flags);
     }
   }
 }
@@ -216,14 +234,14 @@ __device__ __noinline__ uint64_t sample_count_pass(uint32_t* hist, const uint4* 
                                                    int nvec) {
   uint32_t flags = 0, m2 = 0xFF80FF80u;
   int i = threadIdx.x;
-  for (; i + (SM_UNROLL - 1) * SM_THREADS < nvec; i += SM_UNROLL * SM_THREADS) {
+  for (; i + (SM_UNROLL - 1) * sample_nt() < nvec; i += SM_UNROLL * sample_nt()) {
     uint4 v[SM_UNROLL];
 #pragma unroll
-    for (int k = 0; k < SM_UNROLL; ++k) v[k] = z[i + k * SM_THREADS];
+    for (int k = 0; k < SM_UNROLL; ++k) v[k] = z[i + k * sample_nt()];
 #pragma unroll
     for (int k = 0; k < SM_UNROLL; ++k) sample_count8(hist, v[k], m2, flags);
   }
-  for (; i < nvec; i += SM_THREADS) sample_count8(hist, z[i], m2, flags);
+  for (; i < nvec; i += sample_nt()) sample_count8(hist, z[i], m2, flags);
   return m2 | (static_cast<uint64_t>(flags) << 32);
 }
 
@@ -328,7 +346,7 @@ struct SampleKeys {
     __syncthreads();
     if (threadIdx.x < CB) sm.cb[threadIdx.x] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < V; i += SM_THREADS) {
+    for (int i = threadIdx.x; i < V; i += sample_nt()) {
       const uint32_t b = 0xFFFFu - bf16_key(z[i]);
       if (static_cast<int>(b / CB) == chunk && z[i] != 0xFF80u) atomicAdd(&sm.cb[b % CB], 1u);
     }
@@ -532,7 +550,7 @@ __device__ __forceinline__ bool sample_u_ok(float u) { return u >= 0.f && u < 1.
 // Turns the chunks' counts and masses into those before each chunk (the block).
 __device__ __forceinline__ void sample_prefix(SampleShared& sm, uint32_t* pc, double* pw, int n) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per = (n + SM_THREADS - 1) / SM_THREADS;
+  const int per = (n + sample_nt() - 1) / sample_nt();
   const int b = min(n, static_cast<int>(threadIdx.x) * per), e = min(n, b + per);
   uint32_t c = 0;
   double w = 0.0;
@@ -548,8 +566,8 @@ __device__ __forceinline__ void sample_prefix(SampleShared& sm, uint32_t* pc, do
   }
   __syncthreads();
   // every warp scans the warps' sums for itself
-  const uint32_t ca = lane < SM_WARPS ? sm.scan_c[lane] : 0u;
-  const double wa = lane < SM_WARPS ? sm.scan_w[lane] : 0.0;
+  const uint32_t ca = lane < sample_nw() ? sm.scan_c[lane] : 0u;
+  const double wa = lane < sample_nw() ? sm.scan_w[lane] : 0.0;
   const uint32_t cu = warp_scan(ca);
   const double wu = warp_scan(wa);
   c0 += __shfl_sync(0xffffffffu, cu - ca, warp) - c;
@@ -562,7 +580,7 @@ __device__ __forceinline__ void sample_prefix(SampleShared& sm, uint32_t* pc, do
     c0 += ci;
     w0 += wi;
   }
-  if (threadIdx.x == SM_THREADS - 1) {  // lane 31: the sum over all warps
+  if (threadIdx.x == sample_nt() - 1) {  // lane 31: the sum over all warps
     pc[n] = cu;
     pw[n] = wu;
   }
@@ -647,57 +665,103 @@ __device__ __forceinline__ int sample_scan_few(const SampleSpan& sp, const Sampl
   return at + __ffs(__ballot_sync(0xffffffffu, me)) - 1;
 }
 
-// The matches of a value in each tile of `steps` x 32 vectors; returns those in
-// the warp's tiles.
-__device__ __noinline__ uint32_t sample_tiles_pass(uint16_t* tiles, const uint4* __restrict__ z,
-                                                   int nvec, int steps, uint32_t bits) {
+// How often a value occurs among the vectors (the thread's share).
+__device__ __noinline__ uint32_t sample_matches_pass(const uint4* __restrict__ z, int nvec,
+                                                     uint32_t bits) {
   const SampleMatch mt(bits);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int tv = 32 * steps, nt = (nvec + tv - 1) / tv;
-  uint32_t mine = 0;
-  int t = warp;
-  if (steps == 1) {  // whole tiles, SM_UNROLL loads under way
-    for (; t + (SM_UNROLL - 1) * SM_WARPS < nvec / 32; t += SM_UNROLL * SM_WARPS) {
-      uint4 v[SM_UNROLL];
+  uint32_t n = 0;
+  int i = threadIdx.x;
+  for (; i + (SM_UNROLL - 1) * sample_nt() < nvec; i += SM_UNROLL * sample_nt()) {
+    uint4 v[SM_UNROLL];
 #pragma unroll
-      for (int k = 0; k < SM_UNROLL; ++k) v[k] = z[(t + k * SM_WARPS) * 32 + lane];
+    for (int k = 0; k < SM_UNROLL; ++k) v[k] = z[i + k * sample_nt()];
 #pragma unroll
-      for (int k = 0; k < SM_UNROLL; ++k) {
-        const uint32_t n = __reduce_add_sync(0xffffffffu, 8u - __popc(mt.differs8(v[k])));
-        if (lane == 0) tiles[t + k * SM_WARPS] = static_cast<uint16_t>(n);
-        mine += n;
-      }
-    }
+    for (int k = 0; k < SM_UNROLL; ++k) n += 8u - __popc(mt.differs8(v[k]));
   }
-  for (; t < nt; t += SM_WARPS) {
-    uint32_t n = 0;
-    for (int s = 0; s < steps; ++s) {
-      const int i = t * tv + s * 32 + lane;
-      if (i < nvec) n += 8u - __popc(mt.differs8(z[i]));
-    }
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (lane == 0) tiles[t] = static_cast<uint16_t>(n);
-    mine += n;
-  }
-  return mine;
+  for (; i < nvec; i += sample_nt()) n += 8u - __popc(mt.differs8(z[i]));
+  return n;
 }
 
-// Writes the id of one (value, occurrence): the matches in every tile of the
-// block's part are counted, the blocks' counts joined, and the tile that holds
-// the occurrence is read again by the first warp of the block that has it.
+// Writes the id of occurrence `rank` of a value among the vectors, the first of
+// which starts at id `first`; the block goes through them in order, a round of
+// eight tiles of 32 vectors a warp at a time, and stops where it is found.
+// Returns 0xFFFFFFFF, or what is left of the rank if the occurrence is not there.
+__device__ __noinline__ uint32_t sample_find_pass(SampleShared& sm, const uint4* __restrict__ z,
+                                                  int nvec, int first, uint32_t bits,
+                                                  uint32_t rank, int32_t* id_out) {
+  const SampleMatch mt(bits);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int U = SM_TILE_UNROLL;
+  int turn = 0;  // two buffers, so that one barrier a round is enough
+  for (int base = 0; base < nvec; base += 32 * U * sample_nw(), turn ^= 1) {
+    const int i0 = base + warp * 32 * U + lane;
+    uint32_t no[U], n = 0;
+    {
+      uint4 v[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) v[k] = i0 + 32 * k < nvec ? z[i0 + 32 * k] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        no[k] = i0 + 32 * k < nvec ? mt.differs8(v[k]) : SM_EIGHT;
+        n += 8u - __popc(no[k]);
+      }
+    }
+    n = __reduce_add_sync(0xffffffffu, n);
+    uint32_t* sums = turn ? sm.flags : sm.scan_c;
+    if (lane == 0) sums[warp] = n;
+    __syncthreads();
+    const uint32_t mine = lane < sample_nw() ? sums[lane] : 0u;
+    const uint32_t upto = warp_scan(mine);
+    const uint32_t all = __shfl_sync(0xffffffffu, upto, 31);
+    if (rank >= all) {
+      rank -= all;
+      continue;
+    }
+    const int w = __ffs(__ballot_sync(0xffffffffu, upto > rank)) - 1;
+    rank -= __shfl_sync(0xffffffffu, upto - mine, w);
+    if (warp != w) return 0xFFFFFFFFu;
+    bool done = false;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (done) continue;
+      const uint32_t here = 8u - __popc(no[k]);
+      const uint32_t tile = __reduce_add_sync(0xffffffffu, here);
+      if (rank >= tile) {
+        rank -= tile;
+        continue;
+      }
+      done = true;
+      const uint32_t before = warp_scan(here) - here;
+      if (rank >= before && rank < before + here) {  // one lane
+        uint32_t left = rank - before;
+        for (int j = 0; j < 8; ++j) {
+          const bool is = !((no[k] >> ((j & 1) ? 31 - j / 2 : 15 - j / 2)) & 1u);
+          if (is && left-- == 0) {
+            *id_out = first + 8 * (i0 + 32 * k) + j;
+            break;
+          }
+        }
+      }
+    }
+    return 0xFFFFFFFFu;
+  }
+  return rank;
+}
+
+// Writes the id of one (value, occurrence).  In a cluster the blocks count the
+// value in their parts first, and the one that has the occurrence looks for it.
 template <int C>
 __device__ __forceinline__ void sample_find(SampleShared& sm, const SampleSpan& sp, uint32_t rank0,
                                             uint32_t bits, uint32_t rank, int32_t* id_out) {
   const SampleMatch mt(bits);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int steps = max(1, (sp.nvec + 32 * SM_TILES - 1) / (32 * SM_TILES));  // 32 vectors each
-  const int tv = 32 * steps, nt = (sp.nvec + tv - 1) / tv;
-  const uint32_t mine = sample_tiles_pass(sm.tiles, sp.v, sp.nvec, steps, bits);
   if constexpr (C > 1) {
-    if (lane == 0) sm.scan_c[warp] = mine;
+    const uint32_t n =
+        __reduce_add_sync(0xffffffffu, sample_matches_pass(sp.v, sp.nvec, bits));
+    if (lane == 0) sm.scan_c[warp] = n;
     __syncthreads();
     if (warp == 0) {
-      uint32_t all = __reduce_add_sync(0xffffffffu, lane < SM_WARPS ? sm.scan_c[lane] : 0u);
+      uint32_t all = __reduce_add_sync(0xffffffffu, lane < sample_nw() ? sm.scan_c[lane] : 0u);
       const bool few = lane < sp.head ? mt.is(sp.z[lane])
                                       : lane < sp.head + sp.tail &&
                                             mt.is(sp.z[sp.tail_at + lane - sp.head]);
@@ -705,38 +769,20 @@ __device__ __forceinline__ void sample_find(SampleShared& sm, const SampleSpan& 
       if (lane < C) peer_store(peer(&sm.found[rank0][0], lane), all);
     }
     sync_all<C>();
-  } else {
-    __syncthreads();
-  }
-  if (warp != 0) return;
-  if constexpr (C > 1) {
-    uint32_t here = 0;
-    for (uint32_t k = 0; k <= rank0; ++k) {
-      here = sm.found[k][0];
-      if (k == rank0) break;
-      if (rank < here) return;  // in a block before this one
-      rank -= here;
+    for (uint32_t k = 0; k < rank0; ++k) {
+      if (rank < sm.found[k][0]) return;  // in a block before this one
+      rank -= sm.found[k][0];
     }
-    if (rank >= here) return;
+    if (rank >= sm.found[rank0][0]) return;
   }
-  int id = sample_scan_few(sp, mt, 0, sp.head, rank);
-  if (id < 0) {
-    const int per = (nt + 31) / 32;
-    uint32_t sum = 0;
-    for (int i = lane * per; i < min(nt, (lane + 1) * per); ++i) sum += sm.tiles[i];
-    const uint32_t upto = warp_scan(sum);
-    const uint32_t hit = __ballot_sync(0xffffffffu, upto > rank);
-    if (hit == 0) {
-      rank -= __shfl_sync(0xffffffffu, upto, 31);
-      id = sample_scan_few(sp, mt, sp.tail_at, sp.tail, rank);
-    } else {
-      const int l = __ffs(hit) - 1;
-      rank -= __shfl_sync(0xffffffffu, upto - sum, l);
-      int t = l * per;
-      while (rank >= sm.tiles[t]) rank -= sm.tiles[t++];
-      id = sample_scan(sp, mt, t * tv, min(sp.nvec, (t + 1) * tv), rank);
-    }
+  const int few = sample_scan_few(sp, mt, 0, sp.head, rank);
+  if (few >= 0) {
+    if (threadIdx.x == 0) *id_out = few;
+    return;
   }
+  rank = sample_find_pass(sm, sp.v, sp.nvec, sp.first, bits, rank, id_out);
+  if (rank == 0xFFFFFFFFu || warp != 0) return;
+  const int id = sample_scan_few(sp, mt, sp.tail_at, sp.tail, rank);
   if (lane == 0) *id_out = id;
 }
 
@@ -775,14 +821,14 @@ __device__ __forceinline__ void sample_marked8(SampleShared& sm, const uint4& v,
 __device__ __noinline__ void sample_marked_pass(SampleShared& sm, const uint4* __restrict__ z,
                                                 int nvec, int seg_vecs) {
   int i = threadIdx.x;
-  for (; i + (SM_UNROLL - 1) * SM_THREADS < nvec; i += SM_UNROLL * SM_THREADS) {
+  for (; i + (SM_UNROLL - 1) * sample_nt() < nvec; i += SM_UNROLL * sample_nt()) {
     uint4 v[SM_UNROLL];
 #pragma unroll
-    for (int k = 0; k < SM_UNROLL; ++k) v[k] = z[i + k * SM_THREADS];
+    for (int k = 0; k < SM_UNROLL; ++k) v[k] = z[i + k * sample_nt()];
 #pragma unroll
-    for (int k = 0; k < SM_UNROLL; ++k) sample_marked8(sm, v[k], (i + k * SM_THREADS) / seg_vecs);
+    for (int k = 0; k < SM_UNROLL; ++k) sample_marked8(sm, v[k], (i + k * sample_nt()) / seg_vecs);
   }
-  for (; i < nvec; i += SM_THREADS) sample_marked8(sm, z[i], i / seg_vecs);
+  for (; i < nvec; i += sample_nt()) sample_marked8(sm, z[i], i / seg_vecs);
 }
 
 // A row whose finite values are not all covered: the key space in eight
@@ -796,11 +842,11 @@ __device__ __noinline__ void sample_row_any(SampleShared& sm, const SampleParams
   bool have = false;
   for (int win = 0; win < 65536 / SM_WIN; ++win) {
     __syncthreads();
-    for (int i = tid; i < SM_WIN; i += SM_THREADS) sm.hist[i] = 0;
-    if (tid < SM_WARPS) sm.flags[tid] = 0xFFFFFFFFu;
+    for (int i = tid; i < SM_WIN; i += sample_nt()) sm.hist[i] = 0;
+    if (tid < sample_nw()) sm.flags[tid] = 0xFFFFFFFFu;
     __syncthreads();
     uint32_t top = 0xFFFFFFFFu;  // the first bin of the window that occurs
-    for (int i = tid; i < p.V; i += SM_THREADS) {
+    for (int i = tid; i < p.V; i += sample_nt()) {
       const uint32_t x = z[i], b = 0xFFFFu - bf16_key(x);
       if (static_cast<int>(b / SM_WIN) == win && x != 0xFF80u) {
         atomicAdd(&sm.hist[b % SM_WIN], 1u);
@@ -810,12 +856,12 @@ __device__ __noinline__ void sample_row_any(SampleShared& sm, const SampleParams
     top = __reduce_min_sync(0xffffffffu, top);
     if (lane == 0) sm.flags[warp] = top;
     __syncthreads();
-    for (int w = 0; w < SM_WARPS; ++w) top = min(top, sm.flags[w]);
+    for (int w = 0; w < sample_nw(); ++w) top = min(top, sm.flags[w]);
     if (!have && top != 0xFFFFFFFFu) {
       m = s.value(static_cast<int>(top));
       have = true;
     }
-    for (int c = warp; c < SM_WIN / 32; c += SM_WARPS) {
+    for (int c = warp; c < SM_WIN / 32; c += sample_nw()) {
       const uint32_t n = sm.hist[c * 32 + lane];
       const int b = win * SM_WIN + c * 32 + lane;
       const double w = warp_sum(n ? n * sample_weight(s.value(b), m, r) : 0.0);
@@ -882,7 +928,7 @@ template <int C>
 __device__ __noinline__ void sample_chunks(SampleShared& sm, uint32_t rank, float m) {
   const SampleRow r = sm.par;
   static_assert(SM_CB == 16, "four lanes a chunk, four bins each");
-  constexpr int PER = SM_THREADS / 4;  // chunks of a pass
+  const int PER = sample_nt() / 4;  // chunks of a pass
   const int sub = threadIdx.x & 3;
   for (int k0 = 0; k0 * C < SM_CHUNKS; k0 += PER) {  // whole warps: lanes add up below
     const int c = rank + C * (k0 + static_cast<int>(threadIdx.x) / 4);
@@ -975,8 +1021,8 @@ __device__ __noinline__ void sample_batch(SampleShared& sm, const SampleParams& 
       }
     }
   }
-  for (int i = tid; i < SM_SEGS * SM_BATCH / 2; i += SM_THREADS) (&sm.segs[0][0])[i] = 0;
-  for (int i = tid; i < 65536 / 32; i += SM_THREADS) sm.drawn[i] = 0;
+  for (int i = tid; i < SM_SEGS * SM_BATCH / 2; i += sample_nt()) (&sm.segs[0][0])[i] = 0;
+  for (int i = tid; i < 65536 / 32; i += sample_nt()) sm.drawn[i] = 0;
   sync_all<C>();  // no block reads another's counters any more
   // mark: 0x80000000 | the draw whose column counts the value; the count
   // itself is kept by the draw's thread and put back behind the pass
@@ -999,7 +1045,7 @@ __device__ __noinline__ void sample_batch(SampleShared& sm, const SampleParams& 
     return (sm.segs[seg][col >> 1] >> ((col & 1u) * 16u)) & 0xFFFFu;
   };
   if constexpr (C > 1) {  // how often this block has each drawn value
-    for (int n = warp; n < nb; n += SM_WARPS) {
+    for (int n = warp; n < nb; n += sample_nw()) {
       const uint32_t bin = sm.draw_bin[n];
       if (bin == 0xFFFFFFFFu) continue;
       const uint32_t col = sm.hist[sample_bin_slot(static_cast<int>(bin))] & (SM_BATCH - 1u);
@@ -1015,7 +1061,7 @@ __device__ __noinline__ void sample_batch(SampleShared& sm, const SampleParams& 
     }
     sync_all<C>();
   }
-  for (int n = warp; n < nb; n += SM_WARPS) {
+  for (int n = warp; n < nb; n += sample_nw()) {
     const uint32_t bin = sm.draw_bin[n];
     if (bin == 0xFFFFFFFFu) continue;
     const uint32_t col = sm.hist[sample_bin_slot(static_cast<int>(bin))] & (SM_BATCH - 1u);
@@ -1065,8 +1111,8 @@ __device__ __noinline__ void sample_batch(SampleShared& sm, const SampleParams& 
   sync_all<C>();  // the counters are as they were, for the next draws
 }
 
-template <int C>
-__global__ void __launch_bounds__(SM_THREADS, SM_BLOCKS) sample_kernel(const __grid_constant__ SampleParams p) {
+template <int C, bool MANY>
+__global__ void __launch_bounds__(sample_threads(MANY), sample_blocks(MANY)) sample_kernel(const __grid_constant__ SampleParams p) {
   extern __shared__ __align__(16) uint8_t sample_smem[];
   SampleShared& sm = *reinterpret_cast<SampleShared*>(sample_smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -1075,7 +1121,7 @@ __global__ void __launch_bounds__(SM_THREADS, SM_BLOCKS) sample_kernel(const __g
     const SampleSpan sp(p.logits + row * p.ld, p.V, C, rank);
     sync_all<C>();  // the last row's reads of shared memory
     if (tid == 0) sm.par = sample_row_params(p, row);
-    for (int i = tid; i < SM_BINS / 4; i += SM_THREADS)
+    for (int i = tid; i < SM_BINS / 4; i += sample_nt())
       reinterpret_cast<uint4*>(sm.hist)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
 
@@ -1097,7 +1143,7 @@ __global__ void __launch_bounds__(SM_THREADS, SM_BLOCKS) sample_kernel(const __g
       sm.flags[warp] = flags;
     }
     __syncthreads();
-    for (int w = 0; w < SM_WARPS; ++w) {
+    for (int w = 0; w < sample_nw(); ++w) {
       m = fmaxf(m, sm.red[w]);
       flags |= sm.flags[w];
     }
@@ -1120,7 +1166,7 @@ __global__ void __launch_bounds__(SM_THREADS, SM_BLOCKS) sample_kernel(const __g
     const bool bad = !r.ok || (flags & SF_BAD);
     if (bad || m == -INFINITY) {  // no answer: bad numbers, or nothing left to draw
       if (rank == 0)
-        for (int n = tid; n < p.N; n += SM_THREADS) sample_no_draw(p, row, n);
+        for (int n = tid; n < p.N; n += sample_nt()) sample_no_draw(p, row, n);
       if (bad && rank == 0 && tid == 0) sample_bad(p);
       continue;
     }
@@ -1143,7 +1189,7 @@ __global__ void __launch_bounds__(SM_THREADS, SM_BLOCKS) sample_kernel(const __g
       const SampleBins<C> s{sm};
       double mass;
       const uint32_t L = sample_kept(s, m, r, mass);
-      if (p.N == 1) {
+      if constexpr (!MANY) {
         const float u = p.u[row];
         const bool ok = sample_u_ok(u);
         const SamplePlace d = sample_draw(s, m, r, L, mass, ok ? u : 0.f);
@@ -1159,7 +1205,10 @@ __global__ void __launch_bounds__(SM_THREADS, SM_BLOCKS) sample_kernel(const __g
       }
     }
     __syncthreads();
-    if (p.N == 1) {
+    if constexpr (MANY) {
+      for (int n0 = 0; n0 < p.N; n0 += SM_BATCH)
+        sample_batch<C>(sm, p, row, sp, rank, m, n0);
+    } else {
       const uint32_t bin = sm.draw_bin[0];
       if (bin == 0xFFFFFFFFu) {
         if (rank == 0 && tid == 0) {
@@ -1172,10 +1221,7 @@ __global__ void __launch_bounds__(SM_THREADS, SM_BLOCKS) sample_kernel(const __g
         p.logp[row] = static_cast<float>(log(sm.draw_w / sm.mass));
       sample_find<C>(sm, sp, rank, sample_bin_bits(static_cast<int>(bin)), sm.draw_rank[0],
                      p.ids + row);
-      continue;
     }
-    for (int n0 = 0; n0 < p.N; n0 += SM_BATCH)
-      sample_batch<C>(sm, p, row, sp, rank, m, n0);
   }
   if constexpr (C > 1) sync_all<C>();  // no block leaves while another reads its counters
 }
