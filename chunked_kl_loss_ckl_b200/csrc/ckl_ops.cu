@@ -241,14 +241,15 @@ int sample_launch(const ckl::SampleParams& p, int sms, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, k, p) == cudaSuccess ? CKL_OK : CKL_ERR_CUDA;
 }
 
-// Blocks a row: as many as two blocks an SM hold at a time (of 512 threads not
-// quite: clusters have to fit into groups of SMs, 74 of four do not, 64 do).
+// Blocks a row: as many as give every SM one.  Clusters of 8 and 4 have to fit
+// into groups of SMs and do so to about 7/8.  128256 logits, one draw, us with
+// 1 / 2 / 4 / 8 blocks: 8 rows 34 / 28 / 23 / 20, 28 rows 35 / 29 / 23 / 26,
+// 64 rows 35 / 30 / 28 / 53, 148 rows 35 / 36 / 57 / 99; 96 rows of 201088 53 / 48.
 template <bool MANY>
 int sample_rows(const ckl::SampleParams& p, int sms, cudaStream_t st) {
-  const int64_t places = MANY ? static_cast<int64_t>(sms) * 7 / 4 : static_cast<int64_t>(sms) * 2;
-  if (p.T * 8 <= places) return sample_launch<8, MANY>(p, sms, st);
-  if (p.T * 4 <= places) return sample_launch<4, MANY>(p, sms, st);
-  if (p.T * 2 <= places) return sample_launch<2, MANY>(p, sms, st);
+  if (p.T * 8 <= sms * 7 / 8) return sample_launch<8, MANY>(p, sms, st);
+  if (p.T * 4 <= sms * 7 / 8) return sample_launch<4, MANY>(p, sms, st);
+  if (p.T * 2 <= (MANY ? sms : sms * 3 / 2)) return sample_launch<2, MANY>(p, sms, st);
   return sample_launch<1, MANY>(p, sms, st);
 }
 

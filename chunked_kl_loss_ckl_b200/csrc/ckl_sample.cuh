@@ -62,7 +62,7 @@ constexpr int SM_ANY_CB = 32;
 constexpr int SM_ANY_CHUNKS = 65536 / SM_ANY_CB;
 constexpr int SM_SEGS = 128;                    // parts of the row counted per draw
 constexpr int SM_BATCH = 64;                    // draws found in one pass
-static_assert(SM_BATCH <= sample_threads(true), "a draw a thread");
+static_assert(SM_BATCH <= sample_threads(true), "a thread a draw, for the marks");
 
 struct SampleParams {
   const uint16_t* logits;
@@ -315,10 +315,6 @@ struct SampleBins {
   __device__ __forceinline__ uint32_t count(int chunk) const {
     return count_of(chunk * CB + threadIdx.x % CB);
   }
-  // from a chunk's bin to its next, in value
-  __device__ __forceinline__ double gap(int chunk) const {
-    return static_cast<double>(value(chunk * CB + 1)) - static_cast<double>(value(chunk * CB));
-  }
   __device__ __forceinline__ uint32_t count_of(int b) const {
     const uint32_t* at = &sm.hist[sample_bin_slot(b)];
     if constexpr (C == 1) return *at;
@@ -499,11 +495,12 @@ __device__ __forceinline__ SamplePlace sample_draw(const S& s, float m, const Sa
   return p.rank < L && p.w > 0.0 ? p : sample_at_rank(s, m, r, min(p.rank, L - 1));
 }
 
-// A draw a lane, among the first L tokens: the chunk by bisection, then its
-// bins one after another, weights as a geometric series (SampleBins only).
+// A draw by eight lanes, among the first L tokens: the chunk by bisection, then
+// two bins a lane (SampleBins only; the same result in all eight).
 template <typename S>
-__device__ __forceinline__ SamplePlace sample_draw_lane(const S& s, float m, const SampleRow& r,
-                                                        uint32_t L, double mass, float u) {
+__device__ __forceinline__ SamplePlace sample_draw8(const S& s, float m, const SampleRow& r,
+                                                    uint32_t L, double mass, float u) {
+  static_assert(S::CB == 16, "two bins a lane");
   const double target = static_cast<double>(u) * mass;
   int c = 0, hi = S::CHUNKS;  // pw[c] <= target
   while (hi - c > 1) {
@@ -511,35 +508,27 @@ __device__ __forceinline__ SamplePlace sample_draw_lane(const S& s, float m, con
     if (s.pw()[mid] <= target) c = mid;
     else hi = mid;
   }
-  const int b0 = c * S::CB;
-  const double gap = s.gap(c) * r.inv_temp;  // <= 0: from a bin to the next
-  const bool series = gap > -20.0;
-  double w = series ? sample_weight(s.value(b0), m, r) : 0.0;
-  const double ratio = exp(gap);
+  const int lane = threadIdx.x & 31, b = c * S::CB + 2 * (lane & 7);
+  const uint32_t n0 = s.count_of(b), n1 = s.count_of(b + 1);
+  const double w0 = n0 ? sample_weight(s.value(b), m, r) : 0.0;
+  const double w1 = n1 ? sample_weight(s.value(b + 1), m, r) : 0.0;
+  const double x0 = n0 * w0, x = x0 + n1 * w1;
+  const double before = warp_scan<8>(x) - x + s.pw()[c];
+  const uint32_t rank0 = warp_scan<8>(n0 + n1) - (n0 + n1) + s.pc()[c];
+  const uint32_t mine = 0xFFu << (lane & 24);  // the draw's lanes
+  const uint32_t some = __ballot_sync(0xffffffffu, n0 + n1 > 0) & mine;
+  const uint32_t hit = __ballot_sync(0xffffffffu, n0 + n1 > 0 && before + x > target) & mine;
+  // rounding may leave the target behind the chunk's last token
+  const int l = hit ? __ffs(hit) - 1 : some ? 31 - __clz(some) : lane & 24;
+  const bool second = n1 && (n0 == 0 || !(before + x0 > target));
   SamplePlace p;
-  p.bin = b0;
-  p.in_bin = 0;
-  p.mass = s.pw()[c];
-  p.rank = s.pc()[c];  // of the bin's first token
-  double before = p.mass;
-  uint32_t rank = p.rank;
-#pragma unroll 1
-  for (int k = 0; k < S::CB; ++k) {
-    const uint32_t n = s.count_of(b0 + k);
-    if (n) {
-      p.bin = b0 + k;
-      p.rank = rank;
-      p.mass = before;
-      p.in_bin = n;  // for now, its tokens
-      rank += n;
-      before += n * (series ? w : sample_weight(s.value(b0 + k), m, r));
-      if (before > target) break;
-    }
-    w *= ratio;
-  }
-  p.w = sample_weight(s.value(p.bin), m, r);
+  p.bin = __shfl_sync(0xffffffffu, second ? b + 1 : b, l);
+  p.w = __shfl_sync(0xffffffffu, second ? w1 : w0, l);
+  p.mass = __shfl_sync(0xffffffffu, second ? before + x0 : before, l);
+  p.rank = __shfl_sync(0xffffffffu, second ? rank0 + n0 : rank0, l);
+  const uint32_t n = __shfl_sync(0xffffffffu, second ? n1 : n0, l);
   double j = floor((target - p.mass) / p.w);
-  j = fmin(fmax(j, 0.0), p.in_bin ? p.in_bin - 1.0 : 0.0);
+  j = fmin(fmax(j, 0.0), n ? n - 1.0 : 0.0);
   if (p.rank + j >= L) j = fmax(0.0, static_cast<double>(L) - 1.0 - p.rank);  // rounding
   p.in_bin = static_cast<uint32_t>(j);
   return p;
@@ -796,39 +785,47 @@ __device__ __forceinline__ void sample_bad(const SampleParams& p) {
   if (p.status) atomicOr(p.status, CKL_DEV_BAD_SAMPLE);
 }
 
-// Counts those of eight values that were drawn, in part `seg` of the row.  Most
-// were not: a bit for each bf16 pattern says so, which 32 lanes read with few
-// bank conflicts (32 neighbouring values share a word).
-__device__ __forceinline__ void sample_marked8(SampleShared& sm, const uint4& v, int seg) {
+// Bits of those of eight values that were drawn (value j: bit j).  Most were
+// not: a bit for each bf16 pattern says so, which 32 lanes read with few bank
+// conflicts (32 neighbouring values share a word).
+__device__ __forceinline__ uint32_t sample_marked8(const uint32_t* drawn, const uint4& v) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t hits = 0;  // bit j: value j
+  uint32_t hits = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint32_t lo = sm.drawn[(w[j] >> 5) & 0x7FFu], hi = sm.drawn[w[j] >> 21];
+    const uint32_t lo = drawn[(w[j] >> 5) & 0x7FFu], hi = drawn[w[j] >> 21];
     hits |= ((lo >> (w[j] & 31u)) & 1u) << (2 * j);
     hits |= ((hi >> ((w[j] >> 16) & 31u)) & 1u) << (2 * j + 1);
   }
-  while (hits) {
-    const int j = __ffs(hits) - 1;
-    hits &= hits - 1u;
-    const uint32_t word = j < 4 ? (j < 2 ? w[0] : w[1]) : (j < 6 ? w[2] : w[3]);
-    const uint32_t x = (j & 1) ? word >> 16 : word & 0xFFFFu;
-    const uint32_t col = sm.hist[sample_slot_of(x)] & (SM_BATCH - 1u);
-    atomicAdd(&sm.segs[seg][col >> 1], (col & 1u) ? 0x10000u : 1u);
-  }
+  return hits;
 }
 
+// Counts the drawn values in each part (2^shift vectors) of the row.  The lanes
+// go through their hits of SM_UNROLL vectors together: the more elements that
+// is, the nearer the busiest lane is to the mean.
 __device__ __noinline__ void sample_marked_pass(SampleShared& sm, const uint4* __restrict__ z,
-                                                int nvec, int seg_vecs) {
-  int i = threadIdx.x;
-  for (; i + (SM_UNROLL - 1) * sample_nt() < nvec; i += SM_UNROLL * sample_nt()) {
-    uint4 v[SM_UNROLL];
+                                                int nvec, int shift) {
+  static_assert(SM_UNROLL == 4, "32 values, a bit each");
+  for (int i = threadIdx.x; i < nvec; i += SM_UNROLL * sample_nt()) {
+    uint32_t hits = 0;
+    {
+      uint4 v[SM_UNROLL];
 #pragma unroll
-    for (int k = 0; k < SM_UNROLL; ++k) v[k] = z[i + k * sample_nt()];
+      for (int k = 0; k < SM_UNROLL; ++k)
+        v[k] = z[i + k * sample_nt() < nvec ? i + k * sample_nt() : i];
 #pragma unroll
-    for (int k = 0; k < SM_UNROLL; ++k) sample_marked8(sm, v[k], (i + k * sample_nt()) / seg_vecs);
+      for (int k = 0; k < SM_UNROLL; ++k)
+        if (i + k * sample_nt() < nvec) hits |= sample_marked8(sm.drawn, v[k]) << (8 * k);
+    }
+    while (hits) {
+      const int j = __ffs(hits) - 1;
+      hits &= hits - 1u;
+      const int at = i + (j >> 3) * sample_nt();
+      const uint32_t x = reinterpret_cast<const uint16_t*>(z)[8 * at + (j & 7)];
+      const uint32_t col = sm.hist[sample_slot_of(x)] & (SM_BATCH - 1u);
+      atomicAdd(&sm.segs[at >> shift][col >> 1], (col & 1u) ? 0x10000u : 1u);
+    }
   }
-  for (; i < nvec; i += sample_nt()) sample_marked8(sm, z[i], i / seg_vecs);
 }
 
 // A row whose finite values are not all covered: the key space in eight
@@ -1005,19 +1002,22 @@ __device__ __noinline__ void sample_batch(SampleShared& sm, const SampleParams& 
   const uint32_t L = sm.kept;
   const double mass = sm.mass;
   const int nb = min(SM_BATCH, p.N - n0);
-  const int seg_vecs = max(32, ((sp.nvec + SM_SEGS - 1) / SM_SEGS + 31) / 32 * 32);
-  if (tid < nb) {  // a draw a thread
-    const float u = p.u[row * p.N + n0 + tid];
+  int shift = 5;  // a part: the fewest times 32 vectors, a power of two
+  while ((SM_SEGS << shift) < sp.nvec) ++shift;
+  for (int k = 0; k < nb; k += sample_nt() / 8) {  // eight threads a draw
+    const int n = k + tid / 8;
+    const float u = n < nb ? p.u[row * p.N + n0 + n] : 0.f;
     const bool ok = sample_u_ok(u);
-    const SamplePlace d = sample_draw_lane(s, m, r, L, mass, ok ? u : 0.f);
-    sm.draw_bin[tid] = ok ? d.bin : 0xFFFFFFFFu;
-    sm.draw_rank[tid] = d.in_bin;
+    const SamplePlace d = sample_draw8(s, m, r, L, mass, ok ? u : 0.f);
+    if ((tid & 7) != 0 || n >= nb) continue;
+    sm.draw_bin[n] = ok ? d.bin : 0xFFFFFFFFu;
+    sm.draw_rank[n] = d.in_bin;
     if (rank == 0) {
       if (!ok) {
-        sample_no_draw(p, row, n0 + tid);
+        sample_no_draw(p, row, n0 + n);
         sample_bad(p);
       } else if (p.logp) {
-        p.logp[row * p.N + n0 + tid] = static_cast<float>(log(d.w / mass));
+        p.logp[row * p.N + n0 + n] = static_cast<float>(log(d.w / mass));
       }
     }
   }
@@ -1039,7 +1039,7 @@ __device__ __noinline__ void sample_batch(SampleShared& sm, const SampleParams& 
   __syncthreads();
   if (at) atomicMax(at, 0x80000000u | static_cast<uint32_t>(tid));
   __syncthreads();
-  sample_marked_pass(sm, sp.v, sp.nvec, seg_vecs);
+  sample_marked_pass(sm, sp.v, sp.nvec, shift);
   __syncthreads();
   auto in_part = [&](uint32_t seg, uint32_t col) {
     return (sm.segs[seg][col >> 1] >> ((col & 1u) * 16u)) & 0xFFFFu;
@@ -1075,7 +1075,7 @@ __device__ __noinline__ void sample_batch(SampleShared& sm, const SampleParams& 
       }
       if (!here || left >= sm.found[rank][n]) continue;
     }
-    int id = sample_scan_few(sp, mt, 0, sp.head, left);
+    int id = sp.head ? sample_scan_few(sp, mt, 0, sp.head, left) : -1;
     if (id < 0) {
       // lane l: parts 4 l .. 4 l + 3
       uint32_t c[4], sum = 0;
@@ -1101,7 +1101,7 @@ __device__ __noinline__ void sample_batch(SampleShared& sm, const SampleParams& 
           }
         in = __shfl_sync(0xffffffffu, in, l);
         seg = __shfl_sync(0xffffffffu, seg, l);
-        id = sample_scan(sp, mt, seg * seg_vecs, min(sp.nvec, (seg + 1) * seg_vecs), in);
+        id = sample_scan(sp, mt, seg << shift, min(sp.nvec, (seg + 1) << shift), in);
       }
     }
     if (lane == 0) p.ids[row * p.N + n0 + n] = id;
