@@ -230,18 +230,42 @@ __device__ __forceinline__ void sample_count8(uint32_t* hist, const uint4& v, ui
 //
 // Counts the vectors' values; returns the thread's packed maximum and, in the
 // high half, its flags.
+// AHEAD: the next vectors are loaded before these are counted (in the blocks of
+// 256 threads, which have the registers; 4096 x 128256: 567 us without, 552 us
+// so).
+template <bool AHEAD>
 __device__ __noinline__ uint64_t sample_count_pass(uint32_t* hist, const uint4* __restrict__ z,
                                                    int nvec) {
   uint32_t flags = 0, m2 = 0xFF80FF80u;
+  const int step = SM_UNROLL * sample_nt();
   int i = threadIdx.x;
-  for (; i + (SM_UNROLL - 1) * sample_nt() < nvec; i += SM_UNROLL * sample_nt()) {
-    uint4 v[SM_UNROLL];
+  if constexpr (AHEAD) {
+    uint4 v[SM_UNROLL], next[SM_UNROLL];
+    auto load = [&](uint4 (&to)[SM_UNROLL], int at) {
 #pragma unroll
-    for (int k = 0; k < SM_UNROLL; ++k) v[k] = z[i + k * sample_nt()];
+      for (int k = 0; k < SM_UNROLL; ++k)  // -inf is not counted
+        to[k] = at + k * sample_nt() < nvec
+                    ? z[at + k * sample_nt()]
+                    : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
+    };
+    load(v, i);
+    for (; i < nvec; i += step) {
+      load(next, i + step);
 #pragma unroll
-    for (int k = 0; k < SM_UNROLL; ++k) sample_count8(hist, v[k], m2, flags);
+      for (int k = 0; k < SM_UNROLL; ++k) sample_count8(hist, v[k], m2, flags);
+#pragma unroll
+      for (int k = 0; k < SM_UNROLL; ++k) v[k] = next[k];
+    }
+  } else {
+    for (; i + (SM_UNROLL - 1) * sample_nt() < nvec; i += step) {
+      uint4 v[SM_UNROLL];
+#pragma unroll
+      for (int k = 0; k < SM_UNROLL; ++k) v[k] = z[i + k * sample_nt()];
+#pragma unroll
+      for (int k = 0; k < SM_UNROLL; ++k) sample_count8(hist, v[k], m2, flags);
+    }
+    for (; i < nvec; i += sample_nt()) sample_count8(hist, z[i], m2, flags);
   }
-  for (; i < nvec; i += sample_nt()) sample_count8(hist, z[i], m2, flags);
   return m2 | (static_cast<uint64_t>(flags) << 32);
 }
 
@@ -913,7 +937,8 @@ __device__ __forceinline__ SampleRow sample_row_params(const SampleParams& p, in
   r.min_p = p.min_p_rows ? static_cast<double>(p.min_p_rows[row]) : p.min_p;
   r.ok = temp >= 0.0 && temp < INFINITY && r.top_p > 0.0 && r.min_p >= 0.0 && r.min_p <= 1.0;
   r.greedy = temp == 0.0;
-  r.inv_temp = r.greedy ? 1.0 : 1.0 / temp;
+  // finite, so that the largest logit's weight stays exp(0)
+  r.inv_temp = r.greedy ? 1.0 : fmin(1.0 / temp, 1e300);
   return r;
 }
 
@@ -1126,7 +1151,7 @@ __global__ void __launch_bounds__(sample_threads(MANY), sample_blocks(MANY)) sam
     __syncthreads();
 
     // ---- how often each value occurs, and the largest
-    const uint64_t seen = sample_count_pass(sm.hist, sp.v, sp.nvec);
+    const uint64_t seen = sample_count_pass<!MANY>(sm.hist, sp.v, sp.nvec);
     const uint32_t m2 = static_cast<uint32_t>(seen);
     uint32_t flags = static_cast<uint32_t>(seen >> 32);
     float m = fmaxf(bf16_lo(m2), bf16_hi(m2));

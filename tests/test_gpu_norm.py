@@ -256,6 +256,19 @@ def test_other_streams_and_graphs(gpu_lib):
         assert torch.equal(f[0], ref_f[0]) and all(torch.equal(p, q) for p, q in zip(b, ref_b))
 
 
+def test_two_streams_at_once(gpu_lib):
+    x, gamma, beta, dy = _make(2000, 1024, BF, seed=13)
+    f = gpu_lib.norm_forward(x, gamma, beta)
+    ref = gpu_lib.norm_backward(dy, x, f[1], f[2], gamma, bias=True)
+    torch.cuda.synchronize()
+    s = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        got = [gpu_lib.norm_backward(dy, x, f[1], f[2], gamma, bias=True, stream=t) for t in s]
+        torch.cuda.synchronize()
+        for g in got:
+            assert all(torch.equal(a, b) for a, b in zip(g, ref))
+
+
 @pytest.mark.parametrize("checkpoint", [False, True])
 def test_autograd(gpu_lib, checkpoint):
     x, gamma, beta, dy = _make(40, 96, F32, seed=9)
@@ -337,8 +350,8 @@ def test_act8_past_2_31_elements(gpu_lib):
     assert np.array_equal(_np(back[-2:]), val) and not back[:10].any()
 
 
-def test_norm_past_2_31_elements(gpu_lib):
-    T, d = 66000, 32768
+@pytest.mark.parametrize("T,d", [(66000, 32768), (530000, 4096)])
+def test_norm_past_2_31_elements(gpu_lib, T, d):
     x = torch.zeros(T, d, dtype=BF, device="cuda")
     last, gamma, beta, dy = _make(2, d, BF, seed=11)
     x[-2:] = last

@@ -53,7 +53,7 @@ FILTERS = [dict(), dict(temperature=0.7), dict(temperature=1.7), dict(temperatur
            dict(top_k=1), dict(top_k=7), dict(top_k=1000, temperature=1.3), dict(top_p=0.9),
            dict(top_p=1e-6), dict(top_p=0.5, top_k=40), dict(min_p=0.05), dict(min_p=1.0),
            dict(min_p=1e-9), dict(temperature=0.8, top_k=50, top_p=0.95, min_p=0.02),
-           dict(temperature=30.0), dict(temperature=1e-3)]
+           dict(temperature=30.0), dict(temperature=1e-3), dict(temperature=1e-320)]
 
 
 @pytest.mark.parametrize("V", [1, 2, 7, 8, 9, 33, 1000, 1001, 50257])
@@ -208,6 +208,10 @@ def test_wide_rows_and_far_offsets(gpu_lib):
     z, rng = _z(2, 300007, 12)                        # more than one step a tile
     _check(gpu_lib, z, rng.random(2))
     _check(gpu_lib, z, rng.random((2, 70)), top_p=0.95)
+    z = torch.zeros(2, 1 << 21, dtype=BF)             # the widest, all equal: full counters
+    z[1, 5] = 9.0
+    _check(gpu_lib, z, rng.random(2))
+    _check(gpu_lib, z, rng.random((2, 5)))
     big = torch.empty(18 * (1 << 27), dtype=BF, device="cuda").view(18, 1 << 27)
     v = big[:, 7:1007]                                # row 17 starts past 2^31 elements
     z, rng = _z(18, 1000, 13)
@@ -235,6 +239,22 @@ def test_streams_and_graphs(gpu_lib):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(got[0], ref[0]) and torch.equal(one[0], ref[0][:, 0])
+
+
+def test_two_streams_at_once(gpu_lib):
+    # nothing is shared between calls: both draw what they draw alone
+    z, _ = _z(300, 20000, 16)
+    z, u = z.cuda(), torch.rand(300, 70, device="cuda")
+    ref = gpu_lib.sample(z, u, top_p=0.9), gpu_lib.sample(z, u[:, 0].contiguous(), top_k=7)
+    torch.cuda.synchronize()
+    s = [torch.cuda.Stream(), torch.cuda.Stream()]
+    one = u[:, 0].contiguous()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        a = gpu_lib.sample(z, u, top_p=0.9, stream=s[0])
+        b = gpu_lib.sample(z, one, top_k=7, stream=s[1])
+        torch.cuda.synchronize()
+        assert torch.equal(a[0], ref[0][0]) and torch.equal(b[0], ref[1][0])
 
 
 def test_frequencies_follow_the_distribution(gpu_lib):
