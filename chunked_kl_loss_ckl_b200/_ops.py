@@ -207,7 +207,7 @@ def norm_backward(dy, x, mean, rstd, gamma=None, bias: bool = False, dgamma=None
     if isinstance(x, (tuple, list)):
         q, e = x
         _check("q", q, (torch.int8,), dy.shape, like=dy)
-        _check_kept(q, e)
+        _check("exponents", e, (torch.uint8,), _kept_shapes(q.shape)[1], like=dy)
         x = None
     else:
         _check("x", x, (dy.dtype,), dy.shape, like=dy)
