@@ -241,6 +241,18 @@ int sample_launch(const ckl::SampleParams& p, int sms, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, k, p) == cudaSuccess ? CKL_OK : CKL_ERR_CUDA;
 }
 
+template <int E>
+int sample_short(const ckl::SampleParams& p, int sms, cudaStream_t st) {
+  auto* k = ckl::sample_short_kernel<E>;
+  const size_t smem = static_cast<size_t>(ckl::SM_SHORT_THREADS) * E * 12;
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem)) != cudaSuccess)
+    return CKL_ERR_CUDA;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(p.T, static_cast<int64_t>(sms) * 8));
+  k<<<grid, ckl::SM_SHORT_THREADS, smem, st>>>(p);
+  return launched();
+}
+
 // Blocks a row: as many as give every SM one.  Clusters of 8 and 4 have to fit
 // into groups of SMs and do so to about 7/8.  128256 logits, one draw, us with
 // 1 / 2 / 4 / 8 blocks: 8 rows 34 / 28 / 23 / 20, 28 rows 35 / 29 / 23 / 26,
@@ -439,6 +451,14 @@ int ckl_sample(const uint16_t* logits, int64_t ld, int64_t T, int64_t V, const f
   p.logp = logp;
   p.status = device_status;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (V <= (N == 1 ? ckl::SM_SHORT_V : ckl::SM_SHORT_V_MANY)) {
+    const int64_t per = cdiv(V, ckl::SM_SHORT_THREADS);
+    return per == 1   ? sample_short<1>(p, dev.sms, st)
+           : per == 2 ? sample_short<2>(p, dev.sms, st)
+           : per <= 4 ? sample_short<4>(p, dev.sms, st)
+           : per <= 8 ? sample_short<8>(p, dev.sms, st)
+                      : sample_short<16>(p, dev.sms, st);
+  }
   return N == 1 ? sample_rows<false>(p, dev.sms, st) : sample_rows<true>(p, dev.sms, st);
 }
 

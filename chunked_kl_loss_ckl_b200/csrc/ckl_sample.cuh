@@ -1251,4 +1251,196 @@ __global__ void __launch_bounds__(sample_threads(MANY), sample_blocks(MANY)) sam
   if constexpr (C > 1) sync_all<C>();  // no block leaves while another reads its counters
 }
 
+// ------------------------------------------------------------- short rows
+// Rows of up to 4096 logits: sorted whole (value descending, id ascending, one
+// 32-bit word each), with the running masses beside them, so that a draw is a
+// bisection.  The counters' fixed cost a row (12304 of them to clear and to turn
+// into masses, and the search for an occurrence) would be several times the
+// row's own work: 4000 x 1499, 32 draws each, 341 us with them, 128 us so; one
+// draw 136 and 128.  4000 x 4096: 32 draws 345 and 263, one draw 141 and 263, so
+// that form is for rows of up to 2048, and up to 4096 with several draws.
+// A thread holds E neighbours, so that only the last of the sort's steps, over
+// more than a warp's 32 E, go through shared memory (six of 66 at 2048).
+constexpr int SM_SHORT_V = 2048, SM_SHORT_V_MANY = 4096;
+constexpr int SM_SHORT_THREADS = 256;
+constexpr int SM_SHORT_WARPS = SM_SHORT_THREADS / 32;
+
+__device__ __forceinline__ void sample_order(uint32_t& a, uint32_t& b, bool up) {
+  const uint32_t lo = min(a, b), hi = max(a, b);
+  a = up ? lo : hi;
+  b = up ? hi : lo;
+}
+
+// Bitonic sort, ascending, of the block's SM_SHORT_THREADS E words, E a thread.
+template <int E>
+__device__ __forceinline__ void sample_sort(uint32_t (&x)[E], uint32_t* buf0, uint32_t* buf1) {
+  const int tid = threadIdx.x;
+#pragma unroll
+  for (int k = 2; k <= E; k <<= 1) {  // runs of a thread's own
+#pragma unroll
+    for (int j = k / 2; j > 0; j >>= 1)
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if ((e & j) == 0) sample_order(x[e], x[e + j], ((tid * E + e) & k) == 0);
+  }
+#pragma unroll 1
+  for (int t = 2; t <= SM_SHORT_THREADS; t <<= 1) {  // runs of t threads
+    const bool up = (tid & t) == 0;
+#pragma unroll 1
+    for (int d = t / 2; d >= 32; d >>= 1) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) buf0[e * SM_SHORT_THREADS + tid] = x[e];
+      __syncthreads();
+      const bool low = (tid & d) == 0;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const uint32_t y = buf0[e * SM_SHORT_THREADS + (tid ^ d)];
+        x[e] = low == up ? min(x[e], y) : max(x[e], y);
+      }
+      uint32_t* turn = buf0;  // the next step writes the other one: one barrier a step
+      buf0 = buf1;
+      buf1 = turn;
+    }
+#pragma unroll 1
+    for (int d = min(t / 2, 16); d > 0; d >>= 1) {
+      const bool low = (tid & d) == 0;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const uint32_t y = __shfl_xor_sync(0xffffffffu, x[e], d);
+        x[e] = low == up ? min(x[e], y) : max(x[e], y);
+      }
+    }
+#pragma unroll
+    for (int j = E / 2; j > 0; j >>= 1)
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if ((e & j) == 0) sample_order(x[e], x[e + j], up);
+  }
+}
+
+template <int E>
+__global__ void __launch_bounds__(SM_SHORT_THREADS)
+sample_short_kernel(const __grid_constant__ SampleParams p) {
+  constexpr int P = SM_SHORT_THREADS * E;
+  extern __shared__ __align__(16) uint8_t sample_smem[];
+  double* cum = reinterpret_cast<double*>(sample_smem);  // [P] running masses
+  uint32_t* tok = reinterpret_cast<uint32_t*>(cum + P);  // [P] order << 16 | id
+  __shared__ double scan_w[SM_SHORT_WARPS];
+  __shared__ uint32_t scan_n[SM_SHORT_WARPS], scan_k[SM_SHORT_WARPS], scan_f[SM_SHORT_WARPS];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
+    const uint16_t* z = p.logits + row * p.ld;
+    const SampleRow r = sample_row_params(p, row);
+    uint32_t x[E], n = 0, flags = 0;
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+      const int i = k * SM_SHORT_THREADS + tid;
+      x[k] = 0xFFFFFFFFu;  // -inf and what is behind the row: last
+      if (i < p.V) {
+        const uint32_t v = z[i];
+        if ((v & 0x7FFFu) >= 0x7F80u) {
+          if (v != 0xFF80u) flags = SF_BAD;
+        } else {
+          x[k] = (0xFFFFu - bf16_key(v)) << 16 | static_cast<uint32_t>(i);
+          ++n;
+        }
+      }
+    }
+    n = __reduce_add_sync(0xffffffffu, n);
+    flags = __reduce_or_sync(0xffffffffu, flags);
+    __syncthreads();  // the last row's reads of shared memory
+    if (lane == 0) {
+      scan_n[warp] = n;
+      scan_f[warp] = flags;
+    }
+    sample_sort<E>(x, tok, reinterpret_cast<uint32_t*>(cum));
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < E; ++k) tok[tid * E + k] = x[k];
+    __syncthreads();
+    n = 0;
+    for (int w = 0; w < SM_SHORT_WARPS; ++w) {
+      n += scan_n[w];
+      flags |= scan_f[w];
+    }
+    const bool bad = !r.ok || flags;
+    if (bad || n == 0) {
+      for (int k = tid; k < p.N; k += SM_SHORT_THREADS) sample_no_draw(p, row, k);
+      if (bad && tid == 0) sample_bad(p);
+      continue;
+    }
+    auto value = [](uint32_t t) { return key_value(0xFFFFu - (t >> 16)); };
+    const float m = value(tok[0]);
+
+    // running masses: over a thread's tokens, then over the threads
+    double sums[E];
+    uint32_t above = 0;  // tokens with w >= min_p
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+      double w = 0.0;
+      if (tid * E + k < static_cast<int>(n)) {
+        w = sample_weight(value(x[k]), m, r);
+        above += w >= r.min_p;
+      }
+      sums[k] = k ? sums[k - 1] + w : w;
+    }
+    const double upto = warp_scan(sums[E - 1]);
+    above = __reduce_add_sync(0xffffffffu, above);
+    if (lane == 31) {
+      scan_w[warp] = upto;
+      scan_k[warp] = above;
+    }
+    __syncthreads();
+    double before = __shfl_up_sync(0xffffffffu, upto, 1);
+    if (lane == 0) before = 0.0;
+    above = 0;
+    double warps = 0.0;
+    for (int w = 0; w < SM_SHORT_WARPS; ++w) {
+      if (w < warp) warps += scan_w[w];
+      above += scan_k[w];
+    }
+    before += warps;
+#pragma unroll
+    for (int k = 0; k < E; ++k) cum[tid * E + k] = before + sums[k];
+    __syncthreads();
+
+    // the first of [0, count) with past, or count
+    auto first = [&](uint32_t count, auto past) {
+      uint32_t lo = 0, hi = count;
+      while (lo < hi) {
+        const uint32_t mid = (lo + hi) / 2;
+        if (past(cum[mid])) hi = mid;
+        else lo = mid + 1;
+      }
+      return lo;
+    };
+    uint32_t L = n;
+    if (r.greedy) {
+      L = 1;
+    } else {
+      if (r.top_k > 0) L = min(L, static_cast<uint32_t>(r.top_k));
+      uint32_t keep = L;
+      if (r.top_p < 1.0) {
+        const double mass = r.top_p * cum[L - 1];
+        keep = min(keep, first(L, [&](double x) { return x >= mass; }) + 1);
+      }
+      if (r.min_p > 0.0) keep = min(keep, max(1u, above));
+      L = keep;
+    }
+    const double mass = cum[L - 1];
+    for (int k = tid; k < p.N; k += SM_SHORT_THREADS) {
+      const float u = p.u[row * p.N + k];
+      if (!sample_u_ok(u)) {
+        sample_no_draw(p, row, k);
+        sample_bad(p);
+        continue;
+      }
+      const double target = static_cast<double>(u) * mass;
+      const uint32_t at = min(first(L, [&](double x) { return x > target; }), L - 1);
+      sample_put(p, row, k, static_cast<int>(tok[at] & 0xFFFFu),
+                 p.logp ? static_cast<float>(log(sample_weight(value(tok[at]), m, r) / mass)) : 0.f);
+    }
+  }
+}
+
 }  // namespace ckl

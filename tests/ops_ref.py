@@ -68,7 +68,8 @@ def sample(z, u, temperature, top_k, top_p, min_p):
     if temperature == 0:
         w = np.ones(1)
     else:
-        w = np.exp((zs - zs[0]) / temperature)
+        with np.errstate(over="ignore"):
+            w = np.exp((zs - zs[0]) / temperature)
         L = len(w)
         if 0 < top_k < L:
             L = top_k

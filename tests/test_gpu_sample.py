@@ -56,7 +56,7 @@ FILTERS = [dict(), dict(temperature=0.7), dict(temperature=1.7), dict(temperatur
            dict(temperature=30.0), dict(temperature=1e-3), dict(temperature=1e-320)]
 
 
-@pytest.mark.parametrize("V", [1, 2, 7, 8, 9, 33, 1000, 1001, 50257])
+@pytest.mark.parametrize("V", [1, 2, 7, 8, 9, 33, 256, 257, 1001, 2048, 2049, 4096, 4097, 50257])
 def test_every_filter_at_every_size(gpu_lib, V):
     for i, f in enumerate(FILTERS):
         z, rng = _z(5, V, 10 * V + i)
@@ -73,7 +73,7 @@ def test_teacher_sized_rows(gpu_lib, T):
 
 
 @pytest.mark.parametrize("N", [2, 63, 64, 65, 130])
-@pytest.mark.parametrize("V", [5, 999, 128256])
+@pytest.mark.parametrize("V", [5, 999, 4099, 128256])
 def test_many_draws_a_row(gpu_lib, N, V):
     z, rng = _z(3, V, N)
     ids, _ = _check(gpu_lib, z, rng.random((3, N)))
@@ -87,38 +87,44 @@ def test_rows_far_more_than_blocks(gpu_lib):
     _check(gpu_lib, z, rng.random(3000), top_p=0.95)
     z, rng = _z(1500, 300, 2)
     _check(gpu_lib, z, rng.random((1500, 5)))
+    z, rng = _z(1000, 4500, 3)
+    _check(gpu_lib, z, rng.random(1000), top_p=0.95, rows=range(0, 1000, 3))
+    _check(gpu_lib, z, rng.random((1000, 3)), rows=range(0, 1000, 3))
 
 
-def test_ties_and_borders(gpu_lib):
+@pytest.mark.parametrize("V", [1024, 8192])
+def test_ties_and_borders(gpu_lib, V):
     # equal logits: u = k / V is the border of two tokens and draws the second
-    z = torch.full((3, 1024), 0.5, dtype=BF)
+    z = torch.full((3, V), 0.5, dtype=BF)
     z[1] = 0.0
     z[1, ::2] = -0.0                                          # equal to +0
-    z[2, :512] = -1.0
-    u = np.arange(1024) / 1024
+    z[2, :V // 2] = -1.0
+    u = np.arange(V) / V
     ids, logp = _check(gpu_lib, z, np.stack([u, u, u]))
-    assert np.array_equal(ids[0], np.arange(1024)) and np.array_equal(ids[1], np.arange(1024))
-    assert (ids[2, 0] == 512) and np.allclose(logp[0], -np.log(1024))
+    assert np.array_equal(ids[0], np.arange(V)) and np.array_equal(ids[1], np.arange(V))
+    assert (ids[2, 0] == V // 2) and np.allclose(logp[0], -np.log(V))
     # top-k and top-p cut inside a tie: the lowest ids stay
     ids, _ = _check(gpu_lib, z, np.stack([u, u, u]), top_k=3)
-    assert set(ids[0]) == {0, 1, 2} and set(ids[2]) == {512, 513, 514}
+    assert set(ids[0]) == {0, 1, 2} and set(ids[2]) == {V // 2, V // 2 + 1, V // 2 + 2}
     ids, _ = _check(gpu_lib, z, np.stack([u, u, u]), top_p=0.25)
-    assert set(ids[0]) == set(range(256))
+    assert set(ids[0]) == set(range(V // 4))
     rng = np.random.default_rng(3)
-    grid = torch.from_numpy(np.round(rng.normal(0, 2, (40, 2001)) * 2) / 2).to(BF)
+    grid = torch.from_numpy(np.round(rng.normal(0, 2, (40, 2 * V)) * 2) / 2).to(BF)
     for f in (dict(), dict(top_k=11), dict(top_p=0.6), dict(min_p=0.1)):
         _check(gpu_lib, grid, rng.random((40, 4)), **f)
 
 
-def test_ends_of_the_unit_interval(gpu_lib):
-    z, _ = _z(4, 3000, 5)
+@pytest.mark.parametrize("V", [2000, 6000])
+def test_ends_of_the_unit_interval(gpu_lib, V):
+    z, _ = _z(4, V, 5)
     u = np.tile([0.0, 2.0 ** -149, LAST], (4, 1))
     for f in FILTERS:
         _check(gpu_lib, z, u, **f)
 
 
-def test_masked_rows(gpu_lib):
-    z, rng = _z(8, 5003, 6)
+@pytest.mark.parametrize("V", [1003, 5003])
+def test_masked_rows(gpu_lib, V):
+    z, rng = _z(8, V, 6)
     inf, low = float("-inf"), torch.finfo(BF).min
     z[0, 1:] = inf                       # one token left
     z[1] = inf                           # none left
@@ -129,24 +135,26 @@ def test_masked_rows(gpu_lib):
     z[5, 100:] = inf
     z[6, :] = -1e4
     z[6, 3:9] = 2.0
-    z[7, 5002] = inf
+    z[7, V - 1] = inf
     for f in (dict(), dict(top_p=0.9, temperature=0.6), dict(top_k=5), dict(min_p=0.1),
               dict(temperature=0.0), dict(temperature=1e4), dict(temperature=1e38)):
+        _check(gpu_lib, z, rng.random(8), **f)
         ids, _ = _check(gpu_lib, z, rng.random((8, 3)), **f)
         assert (ids[0] == 0).all() and (ids[1] == -1).all()
 
 
-def test_values_of_any_size(gpu_lib):
+@pytest.mark.parametrize("V", [1501, 5001])
+def test_values_of_any_size(gpu_lib, V):
     # beyond the counters' range: tiny, huge, both, and all of the type
     rng = np.random.default_rng(7)
-    z = torch.from_numpy(rng.normal(0, 1, (8, 3001))).to(BF)
+    z = torch.from_numpy(rng.normal(0, 1, (8, V))).to(BF)
     z[0, 5] = 1e-20
-    z[1] = torch.from_numpy(rng.normal(0, 1, 3001) * 1e-30).to(BF)
-    z[2] = torch.from_numpy(rng.normal(0, 1, 3001) * 1e30).to(BF)
-    z[3] = torch.from_numpy(rng.normal(0, 1, 3001) + 300).to(BF)
-    z[4] = torch.from_numpy(rng.normal(0, 1, 3001) - 300).to(BF)
-    z[5] = torch.from_numpy(np.exp(rng.uniform(-80, 80, 3001))
-                            * rng.choice([-1, 1], 3001)).to(BF)
+    z[1] = torch.from_numpy(rng.normal(0, 1, V) * 1e-30).to(BF)
+    z[2] = torch.from_numpy(rng.normal(0, 1, V) * 1e30).to(BF)
+    z[3] = torch.from_numpy(rng.normal(0, 1, V) + 300).to(BF)
+    z[4] = torch.from_numpy(rng.normal(0, 1, V) - 300).to(BF)
+    z[5] = torch.from_numpy(np.exp(rng.uniform(-80, 80, V))
+                            * rng.choice([-1, 1], V)).to(BF)
     z[6, ::3] = -260.0
     z[7, 0] = 256.0
     z[7, 1] = 2.0 ** -133
@@ -157,16 +165,17 @@ def test_values_of_any_size(gpu_lib):
         _check(gpu_lib, z, rng.random((8, 4)), **f)
 
 
-def test_bad_numbers(gpu_lib):
-    z, rng = _z(6, 700, 8)
+@pytest.mark.parametrize("V", [700, 9001])
+def test_bad_numbers(gpu_lib, V):
+    z, rng = _z(6, V, 8)
     z[1, 13] = float("nan")
-    z[2, 699] = float("inf")
+    z[2, V - 1] = float("inf")
     u = rng.random((6, 3))
     u[3, 1], u[4, 0], u[5, 2] = 1.0, -1e-9, np.nan
     ids, _ = _check(gpu_lib, z, u, status=16)
     assert (ids[1] == -1).all() and (ids[2] == -1).all() and (ids[3] >= 0).tolist() == [1, 0, 1]
     _check(gpu_lib, z, u[:, 2], status=16)
-    z, _ = _z(6, 700, 9)
+    z, _ = _z(6, V, 9)
     bad = float("nan")
     _check(gpu_lib, z, rng.random(6), status=16,
            temperature=torch.tensor([1.0, -1.0, bad, float("inf"), 1.0, 0.0]))
@@ -174,8 +183,9 @@ def test_bad_numbers(gpu_lib):
     _check(gpu_lib, z, rng.random(6), status=16, min_p=torch.tensor([0.0, -0.1, 1.1, bad, 1.0, 0.5]))
 
 
-def test_parameters_per_row(gpu_lib):
-    z, rng = _z(24, 4001, 10)
+@pytest.mark.parametrize("V", [1700, 7001])
+def test_parameters_per_row(gpu_lib, V):
+    z, rng = _z(24, V, 10)
     pick = lambda v, dt: torch.tensor(rng.choice(v, 24), dtype=dt)  # noqa: E731
     for _ in range(3):
         _check(gpu_lib, z, rng.random((24, 2)),
@@ -185,11 +195,12 @@ def test_parameters_per_row(gpu_lib):
                min_p=pick([0.0, 0.05, 0.5], torch.float32))
 
 
-def test_strided_rows_bit_types_and_repeats(gpu_lib):
-    z, rng = _z(13, 1003, 11)
-    wide = torch.full((13, 1009), 50.0, dtype=BF, device="cuda")  # beside the rows: large
+@pytest.mark.parametrize("V", [1003, 5003])
+def test_strided_rows_bit_types_and_repeats(gpu_lib, V):
+    z, rng = _z(13, V, 11)
+    wide = torch.full((13, V + 6), 50.0, dtype=BF, device="cuda")  # beside the rows: large
     for at in (0, 1, 5):
-        v = wide[:, at:at + 1003]
+        v = wide[:, at:at + V]
         v.copy_(z)
         u = torch.from_numpy(rng.random((13, 9))).float()
         _check(gpu_lib, v, u)
@@ -213,10 +224,11 @@ def test_wide_rows_and_far_offsets(gpu_lib):
     _check(gpu_lib, z, rng.random(2))
     _check(gpu_lib, z, rng.random((2, 5)))
     big = torch.empty(18 * (1 << 27), dtype=BF, device="cuda").view(18, 1 << 27)
-    v = big[:, 7:1007]                                # row 17 starts past 2^31 elements
-    z, rng = _z(18, 1000, 13)
-    v.copy_(z)
-    _check(gpu_lib, v, rng.random(18))
+    for V in (1000, 5000):
+        v = big[:, 7:7 + V]                           # row 17 starts past 2^31 elements
+        z, rng = _z(18, V, 13)
+        v.copy_(z)
+        _check(gpu_lib, v, rng.random(18))
 
 
 def test_streams_and_graphs(gpu_lib):
