@@ -133,22 +133,26 @@ int norm_fwd_launch(const ckl::NormFwd& p0, bool vec, int sms, cudaStream_t st) 
                        dim3(rows), ckl::NORM_THREADS, 0, st);
   }
   const dim3 one(static_cast<unsigned>(std::min<int64_t>(p.T, sms)));
-  const dim3 two(static_cast<unsigned>(std::min<int64_t>(p.T, 2 * sms)));
   if (!vec)
     return norm_launch(s.nv == 8 ? ckl::norm_fwd_kernel<TX, 1, 8, false, KEEP>
                                  : ckl::norm_fwd_kernel<TX, 1, 16, false, KEEP>,
-                       p, two, s.threads, 0, st);
+                       p, one, s.threads, 0, st);
   auto go = [&](auto nv) {
     constexpr int NV = decltype(nv)::value, BYTES = ckl::NORM_FWD_BYTES<NV>;
     if constexpr (NV * V <= 16) {
       // the parameters in shared memory where two blocks' fit and groups have
-      // more than a row or two: 16384 x 4096 bf16 58 us with them in
-      // registers, 54 us so
+      // more than a row or two: bf16 16384 x 4096 51 us, 8192 x 5120 37 us (55
+      // and 46 with them in registers, one block an SM); fp32 is within 5 %
+      // either way but for 8192 x 4096 (51 and 42)
       const size_t smem = static_cast<size_t>(s.threads) * BYTES * ckl::norm_fwd_stages(BYTES) +
                           static_cast<size_t>(s.tpr) * NV * V * 8;
-      if (p.T > 2 * sms && smem <= kNormSmem / 2)
-        return norm_launch(ckl::norm_fwd_kernel<TX, V, NV, true, KEEP>, p, two, s.threads, smem,
+      if (p.T > 2 * sms && smem <= kNormSmem / 2) {
+        // 64 registers a thread, 1 KB of shared memory beside a block's own
+        const int64_t fit = std::min<int64_t>(1024 / s.threads, kNormSmem / (smem + 1024));
+        const dim3 all(static_cast<unsigned>(std::min<int64_t>(p.T, sms * std::max<int64_t>(fit, 2))));
+        return norm_launch(ckl::norm_fwd_kernel<TX, V, NV, true, KEEP>, p, all, s.threads, smem,
                            st);
+      }
     }
     return norm_launch(
         ckl::norm_fwd_kernel<TX, V, NV, false, KEEP>, p, one, s.threads,

@@ -23,11 +23,16 @@
 // logit (2^-64 of its weight) that their mass, under 2^-40 of the row's, is
 // never reached by a u of 24 bits.
 //
-// Bound by the adds to shared memory: 32 lanes' random bins meet 3.5 to a bank
-// on average, two cycles each, so 32 logits cost an SM 7 cycles where HBM brings
-// them in 2.7.  Few rows: a row is shared by a cluster of up to 8 blocks, which
-// count their parts, add each other's counters over distributed shared memory
-// and each look for the drawn value in their own part.
+// Bound by the adds to shared memory: 32 lanes' random bins meet 3.5 to a bank,
+// and 32 logits cost an SM 5 cycles where HBM brings them in 2.7; a row of
+// 128256 takes 20 thousand cycles of them, 15 to 20 thousand of fp64 steps that
+// wait on each other (other blocks run meanwhile), and 10 thousand to find the
+// drawn occurrence.  Few rows: a row is shared by a cluster of up to 8 blocks,
+// which count their parts, add each other's counters over distributed shared
+// memory and each look for the drawn value in their own part.  On a B200:
+// 1 x 128256 21 us (fp64 steps and barriers), 96 x 201088 49 us, 4096 x 128256
+// 543 us with one draw a row (1.9 TB/s), 1039 us with 64 (1.0 TB/s: the marks'
+// pass and the searches take as long as the counting).
 #pragma once
 
 #include <cstddef>
@@ -269,11 +274,9 @@ __device__ __noinline__ uint64_t sample_count_pass(uint32_t* hist, const uint4* 
   return m2 | (static_cast<uint64_t>(flags) << 32);
 }
 
-// Over 16 or 32 lanes.
-template <int W = 32>
 __device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
-  for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 // Sum over the lanes up to and with this one.
