@@ -30,8 +30,8 @@
 // drawn occurrence.  Few rows: a row is shared by a cluster of up to 8 blocks,
 // which count their parts, add each other's counters over distributed shared
 // memory and each look for the drawn value in their own part.  On a B200:
-// 1 x 128256 21 us (fp64 steps and barriers), 96 x 201088 49 us, 4096 x 128256
-// 543 us with one draw a row (1.9 TB/s), 1039 us with 64 (1.0 TB/s: the marks'
+// 1 x 128256 16 us (fp64 steps and barriers), 96 x 201088 40 us, 4096 x 128256
+// 533 us with one draw a row (2.0 TB/s), 1020 us with 64 (1.0 TB/s: the marks'
 // pass and the searches take as long as the counting).
 #pragma once
 
@@ -106,12 +106,10 @@ struct alignas(16) SampleShared {
   uint32_t scan_c[SM_MAX_WARPS];
   uint32_t kept;
   uint32_t cb[SM_ANY_CB];  // one chunk's counters (rows of any values)
-  float red[SM_MAX_WARPS];
   uint32_t flags[SM_MAX_WARPS];
-  float row_max;  // of this block's part
-  uint32_t row_flags;
+  uint32_t seen[SM_MAX_CLUSTER * SM_MAX_WARPS];  // each warp's largest key and flags
   uint32_t draw_bin[SM_BATCH], draw_rank[SM_BATCH];
-  uint32_t found[SM_MAX_CLUSTER][SM_BATCH];  // matches of the drawn values in each block's part
+  uint32_t found[SM_MAX_CLUSTER][SM_BATCH];  // how often each block has each drawn value
   union {
     uint32_t any_pc[SM_ANY_CHUNKS + 1];
     struct {                   // many draws; not there in launches for one
@@ -321,13 +319,18 @@ __device__ __forceinline__ void peer_store(uint32_t a, double v) {
   asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(a), "d"(v) : "memory");
 }
 template <int C>
+__device__ __forceinline__ void arrive_all() {
+  if constexpr (C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+template <int C>
+__device__ __forceinline__ void wait_all() {
+  if constexpr (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+template <int C>
 __device__ __forceinline__ void sync_all() {
-  if constexpr (C == 1) {
-    __syncthreads();
-  } else {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  }
+  if constexpr (C == 1) __syncthreads();
+  arrive_all<C>();
+  wait_all<C>();
 }
 
 // The counts of a row, read chunk by chunk: the bins of a row of covered
@@ -681,23 +684,6 @@ __device__ __forceinline__ int sample_scan_few(const SampleSpan& sp, const Sampl
   return at + __ffs(__ballot_sync(0xffffffffu, me)) - 1;
 }
 
-// How often a value occurs among the vectors (the thread's share).
-__device__ __noinline__ uint32_t sample_matches_pass(const uint4* __restrict__ z, int nvec,
-                                                     uint32_t bits) {
-  const SampleMatch mt(bits);
-  uint32_t n = 0;
-  int i = threadIdx.x;
-  for (; i + (SM_UNROLL - 1) * sample_nt() < nvec; i += SM_UNROLL * sample_nt()) {
-    uint4 v[SM_UNROLL];
-#pragma unroll
-    for (int k = 0; k < SM_UNROLL; ++k) v[k] = z[i + k * sample_nt()];
-#pragma unroll
-    for (int k = 0; k < SM_UNROLL; ++k) n += 8u - __popc(mt.differs8(v[k]));
-  }
-  for (; i < nvec; i += sample_nt()) n += 8u - __popc(mt.differs8(z[i]));
-  return n;
-}
-
 // Writes the id of occurrence `rank` of a value among the vectors, the first of
 // which starts at id `first`; the block goes through them in order, a round of
 // eight tiles of 32 vectors a warp at a time, and stops where it is found.
@@ -764,32 +750,20 @@ __device__ __noinline__ uint32_t sample_find_pass(SampleShared& sm, const uint4*
   return rank;
 }
 
-// Writes the id of one (value, occurrence).  In a cluster the blocks count the
-// value in their parts first, and the one that has the occurrence looks for it.
+// Writes the id of one occurrence of a bin's value.  In a cluster the blocks'
+// counters say which of them has it, and that one looks for it.
 template <int C>
 __device__ __forceinline__ void sample_find(SampleShared& sm, const SampleSpan& sp, uint32_t rank0,
-                                            uint32_t bits, uint32_t rank, int32_t* id_out) {
+                                            int bin, uint32_t rank, int32_t* id_out) {
+  const uint32_t bits = sample_bin_bits(bin);
   const SampleMatch mt(bits);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if constexpr (C > 1) {
-    const uint32_t n =
-        __reduce_add_sync(0xffffffffu, sample_matches_pass(sp.v, sp.nvec, bits));
-    if (lane == 0) sm.scan_c[warp] = n;
-    __syncthreads();
-    if (warp == 0) {
-      uint32_t all = __reduce_add_sync(0xffffffffu, lane < sample_nw() ? sm.scan_c[lane] : 0u);
-      const bool few = lane < sp.head ? mt.is(sp.z[lane])
-                                      : lane < sp.head + sp.tail &&
-                                            mt.is(sp.z[sp.tail_at + lane - sp.head]);
-      all += __popc(__ballot_sync(0xffffffffu, few));
-      if (lane < C) peer_store(peer(&sm.found[rank0][0], lane), all);
-    }
-    sync_all<C>();
-    for (uint32_t k = 0; k < rank0; ++k) {
-      if (rank < sm.found[k][0]) return;  // in a block before this one
-      rank -= sm.found[k][0];
-    }
-    if (rank >= sm.found[rank0][0]) return;
+    const uint32_t n = lane < C ? peer_load(peer(&sm.hist[sample_bin_slot(bin)], lane)) : 0u;
+    const uint32_t upto = warp_scan(n);
+    const uint32_t before = __shfl_sync(0xffffffffu, upto - n, rank0);
+    if (rank < before || rank - before >= __shfl_sync(0xffffffffu, n, rank0)) return;
+    rank -= before;
   }
   const int few = sample_scan_few(sp, mt, 0, sp.head, rank);
   if (few >= 0) {
@@ -980,20 +954,28 @@ __device__ __noinline__ void sample_chunks(SampleShared& sm, uint32_t rank, floa
     if (cnt) {
       const uint32_t b0 = slot < SM_HALF ? SM_LO + slot
                                          : slot < SM_NEG ? 0u : 0x8000u + SM_LO + (slot - SM_NEG);
-      const float v0 = bf16_value(b0), v3 = bf16_value(b0 + 3);
-      const double gap = (static_cast<double>(bf16_value(b0 + 1)) - v0) * r.inv_temp;
-      // bin by bin where the largest logit is (its weight is 1 exactly), and at
-      // low temperatures (the series would leave fp64's range)
-      if (fabs(gap) < 20.0 && (m < fminf(v0, v3) || m > fmaxf(v0, v3))) {
-        const double e = sample_weight(bf16_value(b0), m, r), ratio = exp(gap);
-        w = e * (n[0] + ratio * (n[1] + ratio * (n[2] + ratio * n[3])));
-      } else {
-#pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t nk = k < 2 ? (k ? n[1] : n[0]) : (k == 2 ? n[2] : n[3]);
-          if (nk) w += nk * sample_weight(bf16_value(b0 + k), m, r);
-        }
+      const float step = fabsf(bf16_value(b0 + 1) - bf16_value(b0));
+      float top = bf16_value(b0);
+      if (slot < SM_HALF) {  // the largest of positive values is the last
+        top = bf16_value(b0 + 3);
+        uint32_t t = n[0];
+        n[0] = n[3];
+        n[3] = t;
+        t = n[1];
+        n[1] = n[2];
+        n[2] = t;
       }
+      // the bins above the row's largest value are empty; from that value on,
+      // its own weight is 1 exactly
+      for (; top > m; top -= step) {
+        n[0] = n[1];
+        n[1] = n[2];
+        n[2] = n[3];
+        n[3] = 0;
+      }
+      const double e = sample_weight(top, m, r);
+      const double ratio = exp(-static_cast<double>(step) * r.inv_temp);
+      w = e * (n[0] + ratio * (n[1] + ratio * (n[2] + ratio * n[3])));
     }
     cnt += __shfl_xor_sync(0xffffffffu, cnt, 1);
     cnt += __shfl_xor_sync(0xffffffffu, cnt, 2);
@@ -1060,6 +1042,8 @@ __device__ __noinline__ void sample_batch(SampleShared& sm, const SampleParams& 
     const int bin = static_cast<int>(sm.draw_bin[tid]);
     at = &sm.hist[sample_bin_slot(bin)];
     kept = *at;
+    if constexpr (C > 1)
+      for (int b = 0; b < C; ++b) peer_store(peer(&sm.found[rank][tid], b), kept);
     const uint32_t x = sample_bin_bits(bin);
     atomicOr(&sm.drawn[x / 32], 1u << (x % 32));
     if (x == 0u) atomicOr(&sm.drawn[0x8000 / 32], 1u);  // -0
@@ -1068,27 +1052,10 @@ __device__ __noinline__ void sample_batch(SampleShared& sm, const SampleParams& 
   if (at) atomicMax(at, 0x80000000u | static_cast<uint32_t>(tid));
   __syncthreads();
   sample_marked_pass(sm, sp.v, sp.nvec, shift);
-  __syncthreads();
+  sync_all<C>();  // and every block's counts of the drawn values are there
   auto in_part = [&](uint32_t seg, uint32_t col) {
     return (sm.segs[seg][col >> 1] >> ((col & 1u) * 16u)) & 0xFFFFu;
   };
-  if constexpr (C > 1) {  // how often this block has each drawn value
-    for (int n = warp; n < nb; n += sample_nw()) {
-      const uint32_t bin = sm.draw_bin[n];
-      if (bin == 0xFFFFFFFFu) continue;
-      const uint32_t col = sm.hist[sample_bin_slot(static_cast<int>(bin))] & (SM_BATCH - 1u);
-      const SampleMatch mt(sample_bin_bits(static_cast<int>(bin)));
-      const bool few = lane < sp.head ? mt.is(sp.z[lane])
-                                      : lane < sp.head + sp.tail &&
-                                            mt.is(sp.z[sp.tail_at + lane - sp.head]);
-      const uint32_t all =
-          __reduce_add_sync(0xffffffffu, in_part(lane, col) + in_part(lane + 32, col) +
-                                             in_part(lane + 64, col) + in_part(lane + 96, col)) +
-          __popc(__ballot_sync(0xffffffffu, few));
-      if (lane < C) peer_store(peer(&sm.found[rank][n], lane), all);
-    }
-    sync_all<C>();
-  }
   for (int n = warp; n < nb; n += sample_nw()) {
     const uint32_t bin = sm.draw_bin[n];
     if (bin == 0xFFFFFFFFu) continue;
@@ -1147,11 +1114,16 @@ __global__ void __launch_bounds__(sample_threads(MANY), sample_blocks(MANY)) sam
   const uint32_t rank = C == 1 ? 0u : cluster_ctarank();
   for (int64_t row = blockIdx.x / C; row < p.T; row += gridDim.x / C) {
     const SampleSpan sp(p.logits + row * p.ld, p.V, C, rank);
-    sync_all<C>();  // the last row's reads of shared memory
-    if (tid == 0) sm.par = sample_row_params(p, row);
+    const bool first = row == blockIdx.x / C;
+    arrive_all<C>();
+    if (!first) {  // the last row's reads of shared memory
+      wait_all<C>();
+      if constexpr (C == 1) __syncthreads();
+    }
     for (int i = tid; i < SM_BINS / 4; i += sample_nt())
       reinterpret_cast<uint4*>(sm.hist)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
+    if (tid == sample_nt() - 1) sm.par = sample_row_params(p, row);
 
     // ---- how often each value occurs, and the largest
     const uint64_t seen = sample_count_pass<!MANY>(sm.hist, sp.v, sp.nvec);
@@ -1163,31 +1135,25 @@ __global__ void __launch_bounds__(sample_threads(MANY), sample_blocks(MANY)) sam
       sample_count1(sm.hist, x, flags);
       m = fmaxf(m, bf16_value(x));
     }
+    // every warp's, to all blocks
+    const uint32_t key =
+        (__reduce_max_sync(0xffffffffu, bf16_key(__float_as_uint(m) >> 16)) << 16) |
+        __reduce_or_sync(0xffffffffu, flags);
+    if (first) wait_all<C>();  // the other blocks run by now
+    if constexpr (C == 1) {
+      if (lane == 0) sm.seen[warp] = key;
+    } else {
+      if (lane < C) peer_store(peer(&sm.seen[rank * sample_nw() + warp], lane), key);
+    }
+    sync_all<C>();
+    uint32_t top = 0;
+    flags = 0;
+    for (int i = lane; i < C * sample_nw(); i += 32) {
+      top = max(top, sm.seen[i] >> 16);
+      flags |= sm.seen[i] & 0xFFFFu;
+    }
+    m = key_value(__reduce_max_sync(0xffffffffu, top));  // -0 is +0
     flags = __reduce_or_sync(0xffffffffu, flags);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) {
-      sm.red[warp] = m;
-      sm.flags[warp] = flags;
-    }
-    __syncthreads();
-    for (int w = 0; w < sample_nw(); ++w) {
-      m = fmaxf(m, sm.red[w]);
-      flags |= sm.flags[w];
-    }
-    if constexpr (C > 1) {
-      if (tid == 0) {
-        sm.row_max = m;
-        sm.row_flags = flags;
-      }
-      sync_all<C>();
-#pragma unroll
-      for (int b = 0; b < C; ++b) {
-        m = fmaxf(m, __uint_as_float(peer_load(peer(&sm.row_max, b))));
-        flags |= peer_load(peer(&sm.row_flags, b));
-      }
-    }
-    if (m == 0.f) m = 0.f;  // -0 counts as +0
 
     // the rest is decided alike in all blocks of the row
     const SampleRow& r = sm.par;
@@ -1247,8 +1213,7 @@ __global__ void __launch_bounds__(sample_threads(MANY), sample_blocks(MANY)) sam
       }
       if (rank == 0 && tid == 32 && p.logp)
         p.logp[row] = static_cast<float>(log(sm.draw_w / sm.mass));
-      sample_find<C>(sm, sp, rank, sample_bin_bits(static_cast<int>(bin)), sm.draw_rank[0],
-                     p.ids + row);
+      sample_find<C>(sm, sp, rank, static_cast<int>(bin), sm.draw_rank[0], p.ids + row);
     }
   }
   if constexpr (C > 1) sync_all<C>();  // no block leaves while another reads its counters
