@@ -257,15 +257,21 @@ int sample_short(const ckl::SampleParams& p, int sms, cudaStream_t st) {
   return launched();
 }
 
-// Blocks a row: as many as give every SM one.  Clusters of 8 and 4 have to fit
-// into groups of SMs and do so to about 7/8.  128256 logits, one draw, us with
-// 1 / 2 / 4 / 8 blocks: 8 rows 34 / 28 / 23 / 20, 28 rows 35 / 29 / 23 / 26,
-// 64 rows 35 / 30 / 28 / 53, 148 rows 35 / 36 / 57 / 99; 96 rows of 201088 53 / 48.
+// Blocks a row: as many as leave every SM one; of long rows with one draw, as
+// many as run at once (three an SM).  Clusters of 4 have to fit into groups of
+// SMs and do so to about 7/8, those of 8 to about 2/3.  us with 1 / 2 / 4 / 8
+// blocks, one draw: 128256 logits 8 rows 33 / 24 / 18 / 16, 16 rows 33 / 24 / 18 /
+// 20, 64 rows 33 / 24 / 23 / 44, 74 rows 33 / 24 / 27 / 45, 148 rows 33 / 29 / 47 /
+// 83, 222 rows 42 / 37 / 82 / 152, 296 rows 43 / 53; 201088 logits 96 rows 46 / 38 /
+// 33 / 55; 32000 logits 32 rows 16 / 16 / 15 / 20, 96 rows 17 / 18 / 24 / 46.  64
+// draws of 128256: 8 rows 49 / 38 / 32 / 30, 32 rows 49 / 39 / 33 / 43, 74 rows 50 /
+// 39 / 69 / 138, 96 rows 50 / 52 / 77 / 145.
 template <bool MANY>
 int sample_rows(const ckl::SampleParams& p, int sms, cudaStream_t st) {
-  if (p.T * 8 <= sms * 7 / 8) return sample_launch<8, MANY>(p, sms, st);
-  if (p.T * 4 <= sms * 7 / 8) return sample_launch<4, MANY>(p, sms, st);
-  if (p.T * 2 <= (MANY ? sms : sms * 3 / 2)) return sample_launch<2, MANY>(p, sms, st);
+  const int64_t at_once = static_cast<int64_t>(sms) * (!MANY && p.V >= 65536 ? 3 : 1);
+  if (p.T * 8 <= sms * 2 / 3) return sample_launch<8, MANY>(p, sms, st);
+  if (p.T * 4 <= at_once * 7 / 8) return sample_launch<4, MANY>(p, sms, st);
+  if (p.T * 2 <= at_once) return sample_launch<2, MANY>(p, sms, st);
   return sample_launch<1, MANY>(p, sms, st);
 }
 

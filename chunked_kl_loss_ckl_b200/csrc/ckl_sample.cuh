@@ -30,7 +30,7 @@
 // drawn occurrence.  Few rows: a row is shared by a cluster of up to 8 blocks,
 // which count their parts, add each other's counters over distributed shared
 // memory and each look for the drawn value in their own part.  On a B200:
-// 1 x 128256 16 us (fp64 steps and barriers), 96 x 201088 40 us, 4096 x 128256
+// 1 x 128256 16 us (fp64 steps and barriers), 96 x 201088 33 us, 4096 x 128256
 // 533 us with one draw a row (2.0 TB/s), 1020 us with 64 (1.0 TB/s: the marks'
 // pass and the searches take as long as the counting).
 #pragma once
