@@ -21,6 +21,7 @@ ACT8_GROUP = 32
 SAMPLE_BAD_INPUT = 16
 
 _DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+_INT32_MAX = 2 ** 31 - 1
 
 
 def _bind(L):
@@ -276,7 +277,11 @@ class _Norm(torch.autograd.Function):
 
 def layer_norm(x, gamma=None, beta=None, eps: float = 1e-5, checkpoint: bool = False):
     """Differentiable layer norm over the last dimension.  With ``checkpoint``
-    the backward pass reads x from 8 bits, and x itself is not kept."""
+    the backward pass reads x from 8 bits, and x itself is not kept.
+
+    To capture both passes into a CUDA graph, take the gradients by
+    ``torch.autograd.grad``, of leaves that no other live autograd graph holds.
+    """
     return _Norm.apply(x, gamma, beta, eps, True, checkpoint)
 
 
@@ -348,6 +353,10 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, stream=Non
     if u.dim() not in (1, 2) or u.shape[0] != T:
         raise ValueError("u must have shape [T] or [T, N]")
     N = 1 if u.dim() == 1 else u.shape[1]
+    if T * N >= _INT32_MAX:
+        raise ValueError("u must have fewer than 2^31 - 1 numbers")
+    if isinstance(top_k, int):  # more than a row has is all of it
+        top_k = max(0, min(top_k, _INT32_MAX))
     numbers, rows = [], []
     for name, v, dt, off in (("temperature", temperature, torch.float32, 1.0),
                              ("top_k", top_k, torch.int32, 0),

@@ -103,3 +103,35 @@ def test_rms_norm_head_and_sampling_from_the_student(gpu_lib):
     ids, lp = ckl.sample(z, u[:, 0].contiguous())
     ref = torch.log_softmax(z.double(), 1).gather(1, ids.long()[:, None])[:, 0]
     assert (lp.double() - ref).abs().max() < 1e-5
+
+
+@pytest.mark.parametrize("checkpoint", [False, True])
+def test_both_passes_captured_by_autograd(gpu_lib, checkpoint):
+    """Forward and backward of the chain in one graph: each replay gives the
+    gradients of what the buffers then hold.  The order of fp32 sums may differ
+    from the eager call's (1000 terms: 2^-14 of the largest), and with it a
+    bf16 rounding (2^-7 of the value)."""
+    ckl = gpu_lib
+    x, gamma, beta, W, teacher, mask, u = _problem(seed=3)
+    idx, logp, _ = ckl.topk_cache(teacher, 24)
+
+    def step(x, gamma, beta, W):
+        leaves = [t.requires_grad_() for t in (x, gamma, beta, W)]
+        H = ckl.layer_norm(*leaves[:3], checkpoint=checkpoint)
+        loss = ckl.chunked_kl_loss(H, leaves[3], idx, logp, mask, chunk=64)
+        return torch.autograd.grad(loss, leaves)
+
+    ref = step(*[t.clone() for t in (x, gamma, beta, W)])
+    held = [torch.zeros_like(t) for t in (x, gamma, beta, W)]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step(*[t.detach() for t in held])
+    for _ in range(2):
+        for h, t in zip(held, (x, gamma, beta, W)):
+            h.copy_(t)
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, ref):
+            a, b = a.double(), b.double()
+            assert ((a - b).abs() <= 2.0 ** -7 * b.abs() + 2.0 ** -14 * b.abs().max()).all()

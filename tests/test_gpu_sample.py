@@ -307,3 +307,12 @@ def test_empty_batch_and_refusals(gpu_lib):
         gpu_lib.sample(z, u, temperature=-1.0)
     with pytest.raises(gpu_lib.CklError):
         gpu_lib.sample(z, torch.empty(4, 0, device="cuda"))
+
+
+def test_counts_past_32_bits_do_not_wrap(gpu_lib):
+    z = _z(3, 5000, 77)[0].cuda()
+    u = torch.rand(3, device="cuda")
+    every = gpu_lib.sample(z, u)
+    for k in (2 ** 31, 2 ** 32 + 1, -1, -2 ** 32 + 1):
+        got = gpu_lib.sample(z, u, top_k=k)
+        assert torch.equal(got[0], every[0]) and torch.equal(got[1], every[1])
