@@ -30,11 +30,11 @@
 // gradients' sums over T get a kernel of their own.
 //
 // On a B200 (share of the copy bandwidth, 6.54 TB/s): forward 16384 x 4096 bf16
-// 51 us (0.80), 4096 x 8192 fp32 43 us (0.96); backward 69 us (0.90); forward
+// 51 us (0.80), 4096 x 8192 fp32 43 us (0.96); backward 68 us (0.91); forward
 // with the 8-bit copy 70 us (0.74); backward from it 75 us (0.69: the bytes'
-// conversion, the issue slots are 61 % taken); backward 4096 x 16384 142 us
-// (0.43: 64 registers).  A row's fixed cost is what short rows pay: backward
-// 131072 x 256 50 us (0.62).  Element-wise rows are bound by instructions: 16384 x
+// conversion, the issue slots are 61 % taken); backward 4096 x 16384 83 us
+// (0.75), from 8 bits 127 us (0.41).  A row's fixed cost is what short rows pay:
+// backward 131072 x 256 50 us (0.62).  Element-wise rows are bound by instructions: 16384 x
 // 1001 bf16 43 us forward (0.23), 45 us backward (0.33).
 #pragma once
 
@@ -44,7 +44,7 @@
 namespace ckl {
 
 constexpr int NORM_THREADS = 512;
-constexpr int NORM_WARPS = 32;  // of a block, at most
+constexpr int NORM_WARPS = 16;  // of a block, at most
 constexpr int NORM_MAX_PARTS = 592;  // blocks whose gradient sums the workspace holds
 
 struct NormFwd {
@@ -95,9 +95,9 @@ __device__ __forceinline__ void cp_async_wait() {
 }
 
 // Stages of a ring whose stage takes `bytes` a thread: as many as fit in 200 KB
-// for the block's threads, four at most.
-__host__ __device__ constexpr int norm_stages(int bytes, int threads) {
-  return 200 * 1024 / (threads * bytes) >= 4 ? 4 : 200 * 1024 / (threads * bytes);
+// for 512 threads, four at most.
+__host__ __device__ constexpr int norm_stages(int bytes) {
+  return 200 * 1024 / (512 * bytes) >= 4 ? 4 : 200 * 1024 / (512 * bytes);
 }
 // Of the forward where two blocks share an SM.
 __host__ __device__ constexpr int norm_fwd_stages(int bytes) { return bytes <= 32 ? 3 : 2; }
@@ -109,8 +109,8 @@ constexpr int NORM_BWD_BYTES = NV * (16 + (Q8 ? VEC16<TX> : 16));
 // What the warps of a row's group tell each other through shared memory: two
 // numbers a warp.  Two buffers take turns, so that one barrier an exchange is
 // enough.  Lane l reads those of warp l mod `span` (4, 8 or 16, at least the
-// row's warps; of two warps where a row has more than 16), so that log2(span)
-// butterfly steps leave a sum over the warps in every lane of a half.
+// row's warps, 16 at most), so that log2(span) butterfly steps leave a sum over
+// the warps in every lane of a half.
 struct RowGroup {
   float2* red;  // [2][NORM_WARPS]
   int buf, warps, span, at, bar, tpr;
@@ -152,7 +152,6 @@ struct RowGroup {
       if ((threadIdx.x & 15) == 0) f[2 * (threadIdx.x >> 5) + hi] = v;
       barrier();
       v = on ? f[2 * at + hi] : 0.f;
-      if (warps > 16 && (threadIdx.x & 15) + 16 < warps) v += f[2 * (at + 16) + hi];
       v = over_warps(v);
       buf ^= NORM_WARPS;
     }
@@ -294,7 +293,7 @@ template <typename TX, int VEC, int NV, bool STAGED, bool KEEP>
 __global__ void __launch_bounds__(NORM_THREADS, STAGED ? 2 : 1) norm_fwd_kernel(const NormFwd p) {
   constexpr int BYTES = NORM_FWD_BYTES<NV>;
   constexpr int S =
-      VEC == 1 ? 1 : STAGED ? norm_fwd_stages(BYTES) : norm_stages(BYTES, NORM_THREADS);
+      VEC == 1 ? 1 : STAGED ? norm_fwd_stages(BYTES) : norm_stages(BYTES);
   using E = typename Lane<VEC>::E;
   constexpr int N = Lane<VEC>::N;
   extern __shared__ __align__(16) uint8_t norm_smem[];
@@ -516,14 +515,21 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_fwd_long_kernel(const NormF
 }
 
 // ------------------------------------------------------------------ backward
-// NT: threads of a block, at most.  1024 of them (rows over 512 threads) have
-// 64 registers each, which hold the gradients' sums but not the row as well:
-// RELOAD reads it from shared memory a second time instead.
-template <typename TX, int VEC, int NV, bool Q8, bool STAGED, int NT>
-__global__ void __launch_bounds__(NT) norm_bwd_kernel(const NormBwd p) {
-  constexpr bool RELOAD = NT > NORM_THREADS;
+// With 32 elements a thread (RELOAD) the gradients' sums take 64 registers, and
+// the row is read from shared memory a second time instead of being held in
+// another 64.
+template <int VEC, int NV>
+constexpr bool NORM_RELOAD = VEC * NV > 16 && VEC > 1;
+template <typename TX, int VEC, int NV, bool Q8>
+__host__ __device__ constexpr int norm_bwd_stages() {
+  return NORM_RELOAD<VEC, NV> ? 2 : norm_stages(NORM_BWD_BYTES<TX, NV, Q8>);
+}
+
+template <typename TX, int VEC, int NV, bool Q8, bool STAGED>
+__global__ void __launch_bounds__(NORM_THREADS) norm_bwd_kernel(const NormBwd p) {
+  constexpr bool RELOAD = NORM_RELOAD<VEC, NV>;
   constexpr int BYTES = NORM_BWD_BYTES<TX, NV, Q8>;
-  constexpr int S = VEC == 1 ? 1 : RELOAD ? 2 : norm_stages(BYTES, NT);
+  constexpr int S = VEC == 1 ? 1 : norm_bwd_stages<TX, VEC, NV, Q8>();
   using E = typename Lane<VEC>::E;
   constexpr int N = Lane<VEC>::N;
   extern __shared__ __align__(16) uint8_t norm_smem[];

@@ -156,7 +156,7 @@ int norm_fwd_launch(const ckl::NormFwd& p0, bool vec, int sms, cudaStream_t st) 
     }
     return norm_launch(
         ckl::norm_fwd_kernel<TX, V, NV, false, KEEP>, p, one, s.threads,
-        static_cast<size_t>(s.threads) * BYTES * ckl::norm_stages(BYTES, ckl::NORM_THREADS), st);
+        static_cast<size_t>(s.threads) * BYTES * ckl::norm_stages(BYTES), st);
   };
   if constexpr (V == 4) {
     if (s.nv == 8) return go(Nv<8>());
@@ -170,42 +170,37 @@ template <typename TX, bool Q8>
 int norm_bwd_launch(const ckl::NormBwd& p0, bool vec, int sms, cudaStream_t st, int& parts) {
   constexpr int V = ckl::VEC16<TX>;
   ckl::NormBwd p = p0;
-  const NormShape s = vec ? norm_shape(p.d, V, 16 / V, 0) : norm_shape(p.d, 1, 8, 16);
+  NormShape s = vec ? norm_shape(p.d, V, 16 / V, 0) : norm_shape(p.d, 1, 8, 16);
+  // bf16 rows of 32 elements a thread: all that 16 do not hold, and from 2560
+  // on where there are rows enough, as more rows are then under way.  us with
+  // 16 / 32 a thread: 32768 x 2880 103 / 93, 8192 x 5120 59 / 49, 16384 x 4096
+  // 68.5 / 67.6, 32768 x 2560 83 / 90, 500 x 4096 9.6 / 11.0.  From 8 bits, which
+  // are converted twice then, 16384 x 4096 75 / 97.
+  if (V == 8 && vec && p.d <= 16384 && (s.nv == 0 || (!Q8 && p.d > 2560 && p.T > 8 * sms)))
+    s = norm_shape(p.d, V, 4, 0);
   p.tpr = s.tpr;
   parts = static_cast<int>(std::min<int64_t>(p.T, std::min(sms, ckl::NORM_MAX_PARTS)));
   const dim3 grid(static_cast<unsigned>(parts));
   const size_t sums = static_cast<size_t>(p.d) * 8;  // a row group's, on the way to the first's
-  auto go = [&](auto nv, auto threads, int tpr) {
-    constexpr int NV = decltype(nv)::value, NT = decltype(threads)::value;
-    constexpr int BYTES = ckl::NORM_BWD_BYTES<TX, NV, Q8>;
-    constexpr int S = NT > ckl::NORM_THREADS ? 2 : ckl::norm_stages(BYTES, NT);
-    const int block = NT / tpr * tpr;
-    const size_t ring = static_cast<size_t>(block) * BYTES * S;
-    const size_t params = static_cast<size_t>(tpr) * NV * V * 4;
+  if (s.nv != 0 && !vec)
+    return norm_launch(s.nv == 8 ? ckl::norm_bwd_kernel<TX, 1, 8, Q8, false>
+                                 : ckl::norm_bwd_kernel<TX, 1, 16, Q8, false>,
+                       p, grid, s.threads, sums, st);
+  auto go = [&](auto nv) {
+    constexpr int NV = decltype(nv)::value;
+    const size_t ring = static_cast<size_t>(s.threads) * ckl::NORM_BWD_BYTES<TX, NV, Q8> *
+                        ckl::norm_bwd_stages<TX, V, NV, Q8>();
+    const size_t params = static_cast<size_t>(s.tpr) * NV * V * 4;
     if (p.T > 2 * sms && ring + params <= kNormSmem)
-      return norm_launch(ckl::norm_bwd_kernel<TX, V, NV, Q8, true, NT>, p, grid, block,
+      return norm_launch(ckl::norm_bwd_kernel<TX, V, NV, Q8, true>, p, grid, s.threads,
                          std::max(ring + params, sums), st);
-    return norm_launch(ckl::norm_bwd_kernel<TX, V, NV, Q8, false, NT>, p, grid, block,
+    return norm_launch(ckl::norm_bwd_kernel<TX, V, NV, Q8, false>, p, grid, s.threads,
                        std::max(ring, sums), st);
   };
-  if (s.nv != 0 && !vec)
-    return norm_launch(s.nv == 8
-                           ? ckl::norm_bwd_kernel<TX, 1, 8, Q8, false, ckl::NORM_THREADS>
-                           : ckl::norm_bwd_kernel<TX, 1, 16, Q8, false, ckl::NORM_THREADS>,
-                       p, grid, s.threads, sums, st);
   if (s.nv != 0) {
-    const Nv<ckl::NORM_THREADS> nt;
-    if constexpr (V == 4) {
-      if (s.nv == 3) return go(Nv<3>(), nt, s.tpr);
-      if (s.nv == 4) return go(Nv<4>(), nt, s.tpr);
-    }
-    return s.nv == 1 ? go(Nv<1>(), nt, s.tpr) : go(Nv<2>(), nt, s.tpr);
-  }
-  if constexpr (V == 8) {
-    if (vec && p.d <= 16384) {  // two vectors for each of up to 1024 threads
-      p.tpr = static_cast<int>(cdiv(p.d, 512) * 32);
-      return go(Nv<2>(), Nv<1024>(), p.tpr);
-    }
+    if constexpr (V == 4)
+      if (s.nv == 3) return go(Nv<3>());
+    return s.nv == 1 ? go(Nv<1>()) : s.nv == 2 ? go(Nv<2>()) : go(Nv<4>());
   }
   parts = static_cast<int>(std::min<int64_t>(cdiv(p.T, 8 * ckl::NORM_COL_WARPS), 64));
   if (p.want_gamma || p.want_beta) {  // first: dx may take dy's place
