@@ -30,12 +30,12 @@
 // gradients' sums over T get a kernel of their own.
 //
 // On a B200 (share of the copy bandwidth, 6.54 TB/s): forward 16384 x 4096 bf16
-// 51 us (0.80), 4096 x 8192 fp32 43 us (0.96); backward 68 us (0.91); forward
-// with the 8-bit copy 70 us (0.74); backward from it 75 us (0.69: the bytes'
-// conversion, the issue slots are 61 % taken); backward 4096 x 16384 83 us
-// (0.75), from 8 bits 127 us (0.41).  A row's fixed cost is what short rows pay:
-// backward 131072 x 256 50 us (0.62).  Element-wise rows are bound by instructions: 16384 x
-// 1001 bf16 43 us forward (0.23), 45 us backward (0.33).
+// 48 us (0.86), 4096 x 8192 fp32 43 to 45 us (0.91 to 0.96); backward 68 us
+// (0.91); forward with the 8-bit copy 63 us (0.82); backward from it 74 us (0.70:
+// the bytes' conversion, the issue slots are 61 % taken); backward 4096 x 16384
+// 83 us (0.75), from 8 bits 127 us (0.41).  A row's fixed cost is what short rows
+// pay: backward 131072 x 256 50 us (0.62).  Element-wise rows are bound by
+// instructions: 16384 x 1001 bf16 43 us forward (0.23), 45 us backward (0.33).
 #pragma once
 
 #include "ckl_act8.cuh"
@@ -288,12 +288,16 @@ __device__ __forceinline__ void norm_keep8(const NormFwd& p, int64_t row, int64_
 //
 // STAGED: gamma and beta in shared memory and 64 registers, so that two blocks
 // run on an SM (the sums are a chain of shuffles that only other warps hide);
-// otherwise they are in registers.  KEEP: x's 8 bits are written too.
+// otherwise they are in registers.  With 32 elements a thread then (RELOAD) the
+// row is read from shared memory for each of its three uses: more rows are
+// under way, and a chain's shuffles are shared by twice the elements.  KEEP:
+// x's 8 bits are written too.
 template <typename TX, int VEC, int NV, bool STAGED, bool KEEP>
 __global__ void __launch_bounds__(NORM_THREADS, STAGED ? 2 : 1) norm_fwd_kernel(const NormFwd p) {
   constexpr int BYTES = NORM_FWD_BYTES<NV>;
   constexpr int S =
       VEC == 1 ? 1 : STAGED ? norm_fwd_stages(BYTES) : norm_stages(BYTES);
+  constexpr bool RELOAD = STAGED && VEC * NV > 16;
   using E = typename Lane<VEC>::E;
   constexpr int N = Lane<VEC>::N;
   extern __shared__ __align__(16) uint8_t norm_smem[];
@@ -373,17 +377,20 @@ __global__ void __launch_bounds__(NORM_THREADS, STAGED ? 2 : 1) norm_fwd_kernel(
   for (; row < p.T; row += stride) {
     Lane<VEC> v[NV];
     uint32_t top[NV];
-    if constexpr (VEC > 1) {
-      fetch(smem_u32(mine) + (off == 0 ? (S - 1) * stage_bytes : off - stage_bytes));
-      cp_async_wait<S - 1>();
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
+    auto get = [&](int i) {
+      if constexpr (VEC > 1) {
         Raw<TX> raw;
         raw.load(mine + off + i * piece);
         raw.get(v[i]);
         if constexpr (KEEP) top[i] = raw.top();
       }
-      off = off == (S - 1) * stage_bytes ? 0 : off + stage_bytes;
+    };
+    if constexpr (VEC > 1) {
+      fetch(smem_u32(mine) + (off == 0 ? (S - 1) * stage_bytes : off - stage_bytes));
+      cp_async_wait<S - 1>();
+      if constexpr (!RELOAD)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) get(i);
     } else {
 #pragma unroll
       for (int i = 0; i < NV; ++i) v[i].e[0] = next[i];
@@ -394,9 +401,11 @@ __global__ void __launch_bounds__(NORM_THREADS, STAGED ? 2 : 1) norm_fwd_kernel(
     if (center) {
       E s = both<E>(0.f);
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
+      for (int i = 0; i < NV; ++i) {
+        if constexpr (RELOAD) get(i);
 #pragma unroll
         for (int j = 0; j < N; ++j) s = vadd(s, v[i].e[j]);
+      }
       mu = vsum(s);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) mu += __shfl_xor_sync(0xffffffffu, mu, o);
@@ -405,6 +414,7 @@ __global__ void __launch_bounds__(NORM_THREADS, STAGED ? 2 : 1) norm_fwd_kernel(
     E ss = both<E>(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
+      if constexpr (RELOAD) get(i);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         E c = vsub(v[i].e[j], both<E>(mu));
@@ -434,6 +444,7 @@ __global__ void __launch_bounds__(NORM_THREADS, STAGED ? 2 : 1) norm_fwd_kernel(
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int col = col0 + i * step;
+      if constexpr (RELOAD) get(i);
       if constexpr (KEEP) norm_keep8<VEC>(p, row, col, on(i), v[i], VEC > 1 ? top[i] : 0u);
       if constexpr (STAGED) {
         norm_staged<VEC>(gs, NV * step, col, g[i]);
@@ -444,6 +455,7 @@ __global__ void __launch_bounds__(NORM_THREADS, STAGED ? 2 : 1) norm_fwd_kernel(
         v[i].e[j] = vfma(vmul(vsub(v[i].e[j], both<E>(mu)), both<E>(rstd)), g[i].e[j], b[i].e[j]);
       if (on(i)) norm_store<TX, VEC>(out + i * step, v[i]);
     }
+    if constexpr (VEC > 1) off = off == (S - 1) * stage_bytes ? 0 : off + stage_bytes;
     out += stride * p.d;
   }
 }

@@ -124,8 +124,12 @@ template <typename TX, bool KEEP>
 int norm_fwd_launch(const ckl::NormFwd& p0, bool vec, int sms, cudaStream_t st) {
   constexpr int V = ckl::VEC16<TX>;
   ckl::NormFwd p = p0;
-  // 16 elements a thread, 32 in long rows
-  const NormShape s = vec ? norm_shape(p.d, V, 16 / V, 32 / V) : norm_shape(p.d, 1, 8, 16);
+  // 16 elements a thread, 32 in long rows; in many bf16 rows from 2560 to what
+  // fits beside gamma and beta, 32 as well.  us with 16 / 32 a thread: 16384 x 4096
+  // 52 / 48 (with the 8-bit copy 70 / 63), 8192 x 6144 45 / 41, 32768 x 2880 76 /
+  // 68 (RMS norm 64 / 68), 32768 x 2560 62 / 63, keeping 8 bits 86 / 98.
+  NormShape s = vec ? norm_shape(p.d, V, 16 / V, 32 / V) : norm_shape(p.d, 1, 8, 16);
+  if (V == 8 && vec && p.d > 2560 && p.d <= 7168 && p.T > 8 * sms) s = norm_shape(p.d, V, 4, 0);
   p.tpr = s.tpr;
   if (s.nv == 0) {
     const unsigned rows = static_cast<unsigned>(std::min<int64_t>(p.T, sms * 4));
@@ -139,11 +143,11 @@ int norm_fwd_launch(const ckl::NormFwd& p0, bool vec, int sms, cudaStream_t st) 
                        p, one, s.threads, 0, st);
   auto go = [&](auto nv) {
     constexpr int NV = decltype(nv)::value, BYTES = ckl::NORM_FWD_BYTES<NV>;
-    if constexpr (NV * V <= 16) {
+    if constexpr (NV * V <= (V == 8 ? 32 : 16)) {
       // the parameters in shared memory where two blocks' fit and groups have
-      // more than a row or two: bf16 16384 x 4096 51 us, 8192 x 5120 37 us (55
-      // and 46 with them in registers, one block an SM); fp32 is within 5 %
-      // either way but for 8192 x 4096 (51 and 42)
+      // more than a row or two: bf16 16 elements a thread 16384 x 4096 51 us,
+      // 8192 x 5120 37 us (55 and 46 with them in registers, one block an SM);
+      // fp32 is within 5 % either way but for 8192 x 4096 (51 and 42)
       const size_t smem = static_cast<size_t>(s.threads) * BYTES * ckl::norm_fwd_stages(BYTES) +
                           static_cast<size_t>(s.tpr) * NV * V * 8;
       if (p.T > 2 * sms && smem <= kNormSmem / 2) {
