@@ -376,8 +376,8 @@ int ckl_norm_backward(const void* dy, int32_t dtype, const void* x, const int8_t
   if (const int rc = ops_device(dev)) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool q8 = x == nullptr;
-  const bool vec = d % static_cast<int64_t>(16 / eb) == 0 && aligned(dy, 16) && aligned(x, 16) && aligned(dx, 16) &&
-                   aligned(gamma, 16) && (!q8 || aligned(q, 8));
+  const bool vec = d % static_cast<int64_t>(16 / eb) == 0 && aligned(dy, 16) && aligned(x, 16) &&
+                   aligned(dx, 16) && aligned(gamma, 16) && (!q8 || aligned(q, 8));
   int parts = 0;
   if (T > 0) {
     ckl::NormBwd p{};

@@ -908,7 +908,8 @@ __device__ __noinline__ void sample_row_any(SampleShared& sm, const SampleParams
 
 __device__ __forceinline__ SampleRow sample_row_params(const SampleParams& p, int64_t row) {
   SampleRow r;
-  const double temp = p.temperature_rows ? static_cast<double>(p.temperature_rows[row]) : p.temperature;
+  const double temp =
+      p.temperature_rows ? static_cast<double>(p.temperature_rows[row]) : p.temperature;
   r.top_k = p.top_k_rows ? p.top_k_rows[row] : p.top_k;
   r.top_p = p.top_p_rows ? static_cast<double>(p.top_p_rows[row]) : p.top_p;
   r.min_p = p.min_p_rows ? static_cast<double>(p.min_p_rows[row]) : p.min_p;
@@ -967,7 +968,7 @@ __device__ __noinline__ void sample_chunks(SampleShared& sm, uint32_t rank, floa
       }
       // the bins above the row's largest value are empty; from that value on,
       // its own weight is 1 exactly
-      for (; top > m; top -= step) {
+      for (int k = 0; k < 3 && top > m; ++k, top -= step) {
         n[0] = n[1];
         n[1] = n[2];
         n[2] = n[3];
@@ -1107,7 +1108,8 @@ __device__ __noinline__ void sample_batch(SampleShared& sm, const SampleParams& 
 }
 
 template <int C, bool MANY>
-__global__ void __launch_bounds__(sample_threads(MANY), sample_blocks(MANY)) sample_kernel(const __grid_constant__ SampleParams p) {
+__global__ void __launch_bounds__(sample_threads(MANY), sample_blocks(MANY))
+sample_kernel(const __grid_constant__ SampleParams p) {
   extern __shared__ __align__(16) uint8_t sample_smem[];
   SampleShared& sm = *reinterpret_cast<SampleShared*>(sample_smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;

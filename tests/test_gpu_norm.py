@@ -113,7 +113,7 @@ def test_forward_and_backward_at_every_width(gpu_lib, d, dtype):
 
 @pytest.mark.parametrize("T,d", [(1, 4096), (149, 2880), (1500, 64), (5000, 8), (3000, 1001),
                                  (700, 4096), (640, 16384), (300, 20000), (300, 9001), (1300, 2880),
-                                 (1205, 5120), (1190, 8192)])
+                                 (1205, 5120), (1190, 8192), (1300, 2568), (1200, 7168), (1200, 7176)])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_many_rows(gpu_lib, T, d, dtype):
     x, gamma, beta, dy = _make(T, d, dtype, seed=1)
