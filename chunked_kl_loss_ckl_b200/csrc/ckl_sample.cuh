@@ -28,8 +28,8 @@
 // 128256 takes 20 thousand cycles of them, 15 to 20 thousand of fp64 steps that
 // wait on each other (other blocks run meanwhile), and 10 thousand to find the
 // drawn occurrence.  Few rows: a row is shared by a cluster of up to 8 blocks,
-// which count their parts, add each other's counters over distributed shared
-// memory and each look for the drawn value in their own part.  On a B200:
+// which count their parts and add each other's counters over distributed shared
+// memory; the one whose part has the drawn occurrence looks for it.  On a B200:
 // 1 x 128256 16 us (fp64 steps and barriers), 96 x 201088 33 us, 4096 x 128256
 // 533 us with one draw a row (2.0 TB/s), 1020 us with 64 (1.0 TB/s: the marks'
 // pass and the searches take as long as the counting).
