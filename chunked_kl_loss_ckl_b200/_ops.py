@@ -319,7 +319,12 @@ def norm_kl_loss(x, gamma, beta, W, idx, logp, mask=None, eps: float = 1e-5, cen
     """``chunked_kl_loss`` of H = norm(x), differentiable in x, gamma, beta and
     W.  Between the passes it keeps x alone: the backward makes H again, as it
     makes the logits again, so T x d hidden states are not held twice."""
-    return _NormKL.apply(x, gamma, beta, W, idx, logp, mask, eps, center, chunk)
+    _check("x", x, (torch.bfloat16,))
+    for name, t in (("W", W), ("topk_idx", idx), ("topk_logp", logp), ("mask", mask)):
+        if t is not None and t.get_device() != x.get_device():
+            raise ValueError(f"{name} is on {t.device}, expected {x.device}")
+    with torch.cuda.device(x.get_device()):
+        return _NormKL.apply(x, gamma, beta, W, idx, logp, mask, eps, center, chunk)
 
 
 # ------------------------------------------------------------------- sampling

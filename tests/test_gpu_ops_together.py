@@ -135,3 +135,22 @@ def test_both_passes_captured_by_autograd(gpu_lib, checkpoint):
         for a, b in zip(got, ref):
             a, b = a.double(), b.double()
             assert ((a - b).abs() <= 2.0 ** -7 * b.abs() + 2.0 ** -14 * b.abs().max()).all()
+
+
+def test_norm_kl_loss_refusals(gpu_lib):
+    ckl = gpu_lib
+    x, gamma, beta, W, teacher, mask, u = _problem(T=8, V=64)
+    idx, logp, _ = ckl.topk_cache(teacher, 4)
+    for bad in ((x.float(), gamma, beta, W, idx, logp, mask),
+                (x, gamma.half(), beta, W, idx, logp, mask)):
+        with pytest.raises(TypeError):
+            ckl.norm_kl_loss(*bad)
+    for bad in ((x.cpu(), gamma, beta, W, idx, logp, mask),
+                (x, gamma, beta, W.cpu(), idx, logp, mask),
+                (x, gamma, beta, W, idx, logp, mask.cpu()),
+                (x, gamma[:-1].contiguous(), beta, W, idx, logp, mask),
+                (x.t(), gamma, beta, W, idx, logp, mask),
+                (x, gamma, beta, W[:, :-8].contiguous(), idx, logp, mask)):
+        with pytest.raises(ValueError):
+            ckl.norm_kl_loss(*bad)
+    assert torch.isfinite(ckl.norm_kl_loss(x, gamma, beta, W, idx, logp, mask))
