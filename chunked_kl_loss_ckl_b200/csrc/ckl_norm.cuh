@@ -431,7 +431,8 @@ __global__ void __launch_bounds__(NORM_THREADS, STAGED ? 2 : 1) norm_fwd_kernel(
       m2 = rg.on ? w.y : 0.f;
       if (center) {
         mu = rg.over_warps(w.x * n_lane) * inv_d;
-        m2 = fmaf((w.x - mu) * (w.x - mu), n_lane, m2);
+        // (a lane without a warp adds nothing, where the square is infinite too)
+        if (rg.on) m2 = fmaf((w.x - mu) * (w.x - mu), n_lane, m2);
       }
       m2 = rg.over_warps(m2);
     }

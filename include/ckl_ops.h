@@ -64,6 +64,7 @@ CKL_API int ckl_act8_unpack(const int8_t* q, const uint8_t* exponents, int64_t T
  *   mean, rstd [T] fp32  out: mu and r, for the backward; mean may be NULL
  *   q, exponents         out: x in 8 bits, for a backward that does not keep
  *                        x (ckl_act8_pack's result); both NULL = none
+ * A row whose (x - mu)^2 add up to more than the largest float gets r = 0.
  * T >= 0, 1 <= d < 2^31 - 2^17, T d < 2^60, eps >= 0 and finite.  Arrays aligned
  * to their elements; rows are taken 16 bytes at a time when they are a multiple
  * of that long and x, y, gamma and beta are 16-byte and q 8-byte aligned.  y may
