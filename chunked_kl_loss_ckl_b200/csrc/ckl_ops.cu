@@ -104,14 +104,18 @@ NormShape norm_shape(int64_t d, int vec, int want, int more) {
   return s;
 }
 
-constexpr size_t kNormSmem = 224 * 1024;  // of an SM, for the blocks' dynamic shared memory
+// Of an SM, for the blocks' dynamic shared memory; also the most a block takes
+// (with the kernels' static part, under 0.5 KB, within the 227 KB that it may).
+constexpr size_t kNormSmem = 224 * 1024;
 
 template <typename P>
 int norm_launch(void (*k)(P), const P& p, dim3 grid, int threads, size_t smem, cudaStream_t st) {
-  // 48 KB, the kernel's static part included, need no opting in
+  // 48 KB, the kernel's static part included, need no opting in.  The limit is
+  // the kernel's, not this call's: every call sets the same one, so that none
+  // lowers what another thread is about to launch with.
   if (smem > 40 * 1024 &&
       cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess)
+                           static_cast<int>(kNormSmem)) != cudaSuccess)
     return CKL_ERR_CUDA;
   k<<<grid, threads, smem, st>>>(p);
   return launched();
