@@ -27,25 +27,50 @@ struct OpsDev {
   int sms = 0, major = 0;
 };
 
+// A runtime call failed: its error is this call's status, and is taken back, as
+// it would be read as a later call's otherwise.
+int failed() {
+  cudaGetLastError();
+  return CKL_ERR_CUDA;
+}
+
+// Status of one launch, whatever errors earlier calls of the process left.
+template <typename... P, typename... A>
+int launch(void (*k)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st,
+           cudaLaunchAttribute* attr, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = attr ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, k, static_cast<P>(args)...) == cudaSuccess ? CKL_OK : failed();
+}
+
+template <typename... P>
+bool allow_smem(void (*k)(P...), size_t bytes) {
+  return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(bytes)) == cudaSuccess;
+}
+
 // CKL_OK, or why the current device cannot be used.
 int ops_device(OpsDev& out) {
   static std::mutex mu;
   static OpsDev cache[64];
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return CKL_ERR_CUDA;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return failed();
   std::lock_guard<std::mutex> lock(mu);
   OpsDev& d = cache[dev];
   if (d.sms == 0 &&
       (cudaDeviceGetAttribute(&d.major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
        cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)) {
     d = OpsDev();
-    return CKL_ERR_CUDA;
+    return failed();
   }
   out = d;
   return d.major == 10 ? CKL_OK : CKL_ERR_UNSUPPORTED;
 }
-
-int launched() { return cudaGetLastError() == cudaSuccess ? CKL_OK : CKL_ERR_CUDA; }
 
 size_t elem_bytes(int32_t dtype) { return dtype == CKL_DTYPE_F32 ? 4 : 2; }
 bool dtype_ok(int32_t dtype) { return dtype == CKL_DTYPE_BF16 || dtype == CKL_DTYPE_F32; }
@@ -65,9 +90,8 @@ int act8_pack_launch(const void* x, int64_t T, int64_t d, int8_t* q, uint8_t* e,
   const unsigned grid = static_cast<unsigned>(
       std::min<int64_t>(cdiv(thr, ckl::ACT8_THREADS), static_cast<int64_t>(sms) * 8));
   auto* k = vec ? ckl::act8_pack_kernel<TX, V> : ckl::act8_pack_kernel<TX, 1>;
-  k<<<grid, ckl::ACT8_THREADS, 0, st>>>(static_cast<const TX*>(x), T, static_cast<int32_t>(d),
-                                        static_cast<int32_t>(groups), q, e);
-  return launched();
+  return launch(k, dim3(grid), ckl::ACT8_THREADS, 0, st, nullptr, static_cast<const TX*>(x), T,
+                static_cast<int32_t>(d), static_cast<int32_t>(groups), q, e);
 }
 
 template <typename TX>
@@ -79,9 +103,8 @@ int act8_unpack_launch(const int8_t* q, const uint8_t* e, int64_t T, int64_t d, 
   const unsigned grid = static_cast<unsigned>(
       std::min<int64_t>(cdiv(thr, ckl::ACT8_THREADS), static_cast<int64_t>(sms) * 8));
   auto* k = vec ? ckl::act8_unpack_kernel<TX, V> : ckl::act8_unpack_kernel<TX, 1>;
-  k<<<grid, ckl::ACT8_THREADS, 0, st>>>(q, e, T, static_cast<int32_t>(d),
-                                        static_cast<int32_t>(groups), static_cast<TX*>(x));
-  return launched();
+  return launch(k, dim3(grid), ckl::ACT8_THREADS, 0, st, nullptr, q, e, T,
+                static_cast<int32_t>(d), static_cast<int32_t>(groups), static_cast<TX*>(x));
 }
 
 // How a norm's rows are taken: `vec` elements a load, `nv` vectors a thread,
@@ -113,12 +136,8 @@ int norm_launch(void (*k)(P), const P& p, dim3 grid, int threads, size_t smem, c
   // 48 KB, the kernel's static part included, need no opting in.  The limit is
   // the kernel's, not this call's: every call sets the same one, so that none
   // lowers what another thread is about to launch with.
-  if (smem > 40 * 1024 &&
-      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(kNormSmem)) != cudaSuccess)
-    return CKL_ERR_CUDA;
-  k<<<grid, threads, smem, st>>>(p);
-  return launched();
+  if (smem > 40 * 1024 && !allow_smem(k, kNormSmem)) return failed();
+  return launch(k, grid, threads, smem, st, nullptr, p);
 }
 
 template <int NV>
@@ -229,35 +248,24 @@ template <int C, bool MANY>
 int sample_launch(const ckl::SampleParams& p, int sms, cudaStream_t st) {
   auto* k = ckl::sample_kernel<C, MANY>;
   const size_t smem = MANY ? sizeof(ckl::SampleShared) : ckl::SM_ONE_BYTES;
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess)
-    return CKL_ERR_CUDA;
+  if (!allow_smem(k, smem)) return failed();
   cudaLaunchAttribute cluster;
   cluster.id = cudaLaunchAttributeClusterDimension;
   cluster.val.clusterDim.x = C;
   cluster.val.clusterDim.y = 1;
   cluster.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
   const int64_t rows = std::max(1, sms * ckl::sample_blocks(MANY) / C);  // at a time
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min(p.T, rows) * C));
-  cfg.blockDim = dim3(ckl::sample_threads(MANY));
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = &cluster;
-  cfg.numAttrs = C > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, k, p) == cudaSuccess ? CKL_OK : CKL_ERR_CUDA;
+  return launch(k, dim3(static_cast<unsigned>(std::min(p.T, rows) * C)), ckl::sample_threads(MANY),
+                smem, st, C > 1 ? &cluster : nullptr, p);
 }
 
 template <int E>
 int sample_short(const ckl::SampleParams& p, int sms, cudaStream_t st) {
   auto* k = ckl::sample_short_kernel<E>;
   const size_t smem = static_cast<size_t>(ckl::SM_SHORT_THREADS) * E * 12;
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess)
-    return CKL_ERR_CUDA;
+  if (!allow_smem(k, smem)) return failed();
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(p.T, static_cast<int64_t>(sms) * 8));
-  k<<<grid, ckl::SM_SHORT_THREADS, smem, st>>>(p);
-  return launched();
+  return launch(k, dim3(grid), ckl::SM_SHORT_THREADS, smem, st, nullptr, p);
 }
 
 // Blocks a row: as many as leave every SM one; of long rows with one draw, as
@@ -412,17 +420,10 @@ int ckl_norm_backward(const void* dy, int32_t dtype, const void* x, const int8_t
   cudaLaunchAttribute early;
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(cdiv(d, ckl::NORM_RED_COLS)), 2);
-  cfg.blockDim = dim3(ckl::NORM_RED_COLS * ckl::NORM_RED_ROWS);
-  cfg.stream = st;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, ckl::norm_reduce_kernel, static_cast<const float*>(workspace),
-                            parts, static_cast<int32_t>(d), dgamma, dbeta, accumulate) ==
-                 cudaSuccess
-             ? CKL_OK
-             : CKL_ERR_CUDA;
+  return launch(ckl::norm_reduce_kernel, dim3(static_cast<unsigned>(cdiv(d, ckl::NORM_RED_COLS)), 2),
+                ckl::NORM_RED_COLS * ckl::NORM_RED_ROWS, 0, st, &early,
+                static_cast<const float*>(workspace), parts, static_cast<int32_t>(d), dgamma, dbeta,
+                accumulate);
 }
 
 int ckl_sample(const uint16_t* logits, int64_t ld, int64_t T, int64_t V, const float* u, int32_t N,
