@@ -20,7 +20,7 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
-inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+constexpr int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
 struct OpsDev {
@@ -116,7 +116,7 @@ struct NormShape {
 // Rows of up to 512 threads with `want` vectors a thread; longer ones `more`
 // vectors (0: the kernels for long rows).  With the threads chosen first, only
 // a thread's last vector may be past the row's end.
-NormShape norm_shape(int64_t d, int vec, int want, int more) {
+constexpr NormShape norm_shape(int64_t d, int vec, int want, int more) {
   NormShape s{vec, 0, 0, 0};
   const int64_t n = cdiv(d, vec);  // vectors of a row
   const int nv = n <= static_cast<int64_t>(ckl::NORM_THREADS) * want ? want : more;
@@ -126,6 +126,81 @@ NormShape norm_shape(int64_t d, int vec, int want, int more) {
   s.threads = ckl::NORM_THREADS / s.tpr * s.tpr;
   return s;
 }
+
+// Forward (V: elements of 16 bytes; many: more rows than 8 an SM): 16 elements a
+// thread, 32 in long rows; in many bf16 rows from 2560 to what fits beside gamma
+// and beta, 32 as well.  us with 16 / 32 a thread: 16384 x 4096 52 / 48 (with the
+// 8-bit copy 70 / 63), 8192 x 6144 45 / 41, 32768 x 2880 76 / 68 (RMS norm 64 /
+// 68), 32768 x 2560 62 / 63, keeping 8 bits 86 / 98.
+constexpr NormShape norm_fwd_shape(int64_t d, int V, bool vec, bool many) {
+  if (!vec) return norm_shape(d, 1, 8, 16);
+  if (V == 8 && many && d > 2560 && d <= 7168) return norm_shape(d, V, 4, 0);
+  return norm_shape(d, V, 16 / V, 32 / V);
+}
+
+// Backward: bf16 rows of 32 elements a thread are all that 16 do not hold, and
+// from 2560 on where there are rows enough, as more rows are then under way.  us
+// with 16 / 32 a thread: 32768 x 2880 103 / 93, 8192 x 5120 59 / 49, 16384 x 4096
+// 68.5 / 67.6, 32768 x 2560 83 / 90, 500 x 4096 9.6 / 11.0.  From 8 bits, which
+// are converted twice then, 16384 x 4096 75 / 97.
+constexpr NormShape norm_bwd_shape(int64_t d, int V, bool vec, bool q8, bool many) {
+  if (!vec) return norm_shape(d, 1, 8, 16);
+  const NormShape s = norm_shape(d, V, 16 / V, 0);
+  if (V == 8 && d <= 16384 && (s.nv == 0 || (!q8 && many && d > 2560)))
+    return norm_shape(d, V, 4, 0);
+  return s;
+}
+
+// Vectors a thread of the kernels that are compiled, and one launch of them.
+template <int... NV>
+struct NormCounts {
+  static constexpr bool has(int nv) { return ((nv == NV) || ...); }
+  template <typename F>
+  static int launch(int nv, F&& go) {
+    int rc = CKL_ERR_UNSUPPORTED;
+    ((nv == NV && (rc = go(std::integral_constant<int, NV>()), true)) || ...);
+    return rc;
+  }
+};
+template <int V>
+using NormFwdCounts = std::conditional_t<V == 8, NormCounts<1, 2, 4>, NormCounts<1, 2, 3, 4, 8>>;
+template <int V>
+using NormBwdCounts = std::conditional_t<V == 8, NormCounts<1, 2, 4>, NormCounts<1, 2, 3, 4>>;
+
+// A kernel takes all of a thread's vectors but the last for granted, so a rule
+// above that gave a width another count, or more than one vector past the row,
+// would read and write behind rows.  Checked for every width that has a shape:
+// moving a threshold to where it would (d = 1280 with four vectors wanted: three)
+// does not compile.
+template <typename Counts>
+constexpr bool norm_shape_ok(const NormShape& s, int64_t n) {
+  return s.nv == 0 || (Counts::has(s.nv) && s.tpr % 32 == 0 && s.tpr <= s.threads &&
+                       s.threads <= ckl::NORM_THREADS && (s.nv - 1) * s.tpr <= n &&
+                       s.nv * s.tpr >= n);
+}
+template <int V>
+constexpr bool norm_fwd_shapes_ok(bool many) {
+  for (int64_t n = 1; n <= 16384 / V + 1; ++n)
+    if (!norm_shape_ok<NormFwdCounts<V>>(norm_fwd_shape(n * V, V, true, many), n)) return false;
+  return true;
+}
+template <int V>
+constexpr bool norm_bwd_shapes_ok(bool q8, bool many) {
+  for (int64_t n = 1; n <= 16384 / V + 1; ++n)
+    if (!norm_shape_ok<NormBwdCounts<V>>(norm_bwd_shape(n * V, V, true, q8, many), n)) return false;
+  return true;
+}
+static_assert(norm_fwd_shapes_ok<8>(false) && norm_fwd_shapes_ok<8>(true), "bf16 forward");
+static_assert(norm_fwd_shapes_ok<4>(false) && norm_fwd_shapes_ok<4>(true), "fp32 forward");
+static_assert(norm_bwd_shapes_ok<8>(false, false) && norm_bwd_shapes_ok<8>(false, true) &&
+                  norm_bwd_shapes_ok<8>(true, false) && norm_bwd_shapes_ok<8>(true, true),
+              "bf16 backward");
+static_assert(norm_bwd_shapes_ok<4>(false, false) && norm_bwd_shapes_ok<4>(false, true) &&
+                  norm_bwd_shapes_ok<4>(true, false) && norm_bwd_shapes_ok<4>(true, true),
+              "fp32 backward");
+static_assert(norm_fwd_shape(16385, 8, true, false).nv == 0 &&
+                  norm_fwd_shape(16388, 4, true, false).nv == 0,
+              "no width behind the checked ones has a shape");
 
 // Of an SM, for the blocks' dynamic shared memory; also the most a block takes
 // (with the kernels' static part, under 0.5 KB, within the 227 KB that it may).
@@ -140,19 +215,11 @@ int norm_launch(void (*k)(P), const P& p, dim3 grid, int threads, size_t smem, c
   return launch(k, grid, threads, smem, st, nullptr, p);
 }
 
-template <int NV>
-using Nv = std::integral_constant<int, NV>;
-
 template <typename TX, bool KEEP>
 int norm_fwd_launch(const ckl::NormFwd& p0, bool vec, int sms, cudaStream_t st) {
   constexpr int V = ckl::VEC16<TX>;
   ckl::NormFwd p = p0;
-  // 16 elements a thread, 32 in long rows; in many bf16 rows from 2560 to what
-  // fits beside gamma and beta, 32 as well.  us with 16 / 32 a thread: 16384 x 4096
-  // 52 / 48 (with the 8-bit copy 70 / 63), 8192 x 6144 45 / 41, 32768 x 2880 76 /
-  // 68 (RMS norm 64 / 68), 32768 x 2560 62 / 63, keeping 8 bits 86 / 98.
-  NormShape s = vec ? norm_shape(p.d, V, 16 / V, 32 / V) : norm_shape(p.d, 1, 8, 16);
-  if (V == 8 && vec && p.d > 2560 && p.d <= 7168 && p.T > 8 * sms) s = norm_shape(p.d, V, 4, 0);
+  const NormShape s = norm_fwd_shape(p.d, V, vec, p.T > 8 * sms);
   p.tpr = s.tpr;
   if (s.nv == 0) {
     const unsigned rows = static_cast<unsigned>(std::min<int64_t>(p.T, sms * 4));
@@ -185,11 +252,7 @@ int norm_fwd_launch(const ckl::NormFwd& p0, bool vec, int sms, cudaStream_t st) 
         ckl::norm_fwd_kernel<TX, V, NV, false, KEEP>, p, one, s.threads,
         static_cast<size_t>(s.threads) * BYTES * ckl::norm_stages(BYTES), st);
   };
-  if constexpr (V == 4) {
-    if (s.nv == 8) return go(Nv<8>());
-    if (s.nv == 3) return go(Nv<3>());
-  }
-  return s.nv == 1 ? go(Nv<1>()) : s.nv == 2 ? go(Nv<2>()) : go(Nv<4>());
+  return NormFwdCounts<V>::launch(s.nv, go);
 }
 
 // Returns the status; `parts` is how many sums the workspace then holds.
@@ -197,14 +260,7 @@ template <typename TX, bool Q8>
 int norm_bwd_launch(const ckl::NormBwd& p0, bool vec, int sms, cudaStream_t st, int& parts) {
   constexpr int V = ckl::VEC16<TX>;
   ckl::NormBwd p = p0;
-  NormShape s = vec ? norm_shape(p.d, V, 16 / V, 0) : norm_shape(p.d, 1, 8, 16);
-  // bf16 rows of 32 elements a thread: all that 16 do not hold, and from 2560
-  // on where there are rows enough, as more rows are then under way.  us with
-  // 16 / 32 a thread: 32768 x 2880 103 / 93, 8192 x 5120 59 / 49, 16384 x 4096
-  // 68.5 / 67.6, 32768 x 2560 83 / 90, 500 x 4096 9.6 / 11.0.  From 8 bits, which
-  // are converted twice then, 16384 x 4096 75 / 97.
-  if (V == 8 && vec && p.d <= 16384 && (s.nv == 0 || (!Q8 && p.d > 2560 && p.T > 8 * sms)))
-    s = norm_shape(p.d, V, 4, 0);
+  const NormShape s = norm_bwd_shape(p.d, V, vec, Q8, p.T > 8 * sms);
   p.tpr = s.tpr;
   parts = static_cast<int>(std::min<int64_t>(p.T, std::min(sms, ckl::NORM_MAX_PARTS)));
   const dim3 grid(static_cast<unsigned>(parts));
@@ -224,11 +280,7 @@ int norm_bwd_launch(const ckl::NormBwd& p0, bool vec, int sms, cudaStream_t st, 
     return norm_launch(ckl::norm_bwd_kernel<TX, V, NV, Q8, false>, p, grid, s.threads,
                        std::max(ring, sums), st);
   };
-  if (s.nv != 0) {
-    if constexpr (V == 4)
-      if (s.nv == 3) return go(Nv<3>());
-    return s.nv == 1 ? go(Nv<1>()) : s.nv == 2 ? go(Nv<2>()) : go(Nv<4>());
-  }
+  if (s.nv != 0) return NormBwdCounts<V>::launch(s.nv, go);
   parts = static_cast<int>(std::min<int64_t>(cdiv(p.T, 8 * ckl::NORM_COL_WARPS), 64));
   if (p.want_gamma || p.want_beta) {  // first: dx may take dy's place
     const dim3 cols(static_cast<unsigned>(cdiv(p.d, 32 * (vec ? V : 1))),

@@ -1,8 +1,12 @@
-"""The norm's forms that rows, parameters and values choose: rows whose squares
-pass the largest float."""
+"""The norm's forms that rows, parameters and values choose: widths around the
+vectors a thread holds, rows whose squares pass the largest float.  Tolerances
+are those of test_gpu_norm.py."""
 
 import pytest
 import torch
+
+import ops_ref
+from test_gpu_norm import _check_backward, _check_forward, _make, _np
 
 pytestmark = pytest.mark.gpu
 
@@ -29,3 +33,14 @@ def test_rows_whose_squares_overflow(gpu_lib, d, dtype):
             assert torch.equal(y[keep], alone[0]) and torch.isfinite(y).all()
             dx, dg, _ = gpu_lib.norm_backward(torch.ones_like(x), x, mean, rstd, gamma)
             assert not dx[1].any() and torch.isfinite(dg).all()
+
+
+@pytest.mark.parametrize("d", [520, 776, 1280, 1288, 1536, 2048, 2056, 2560, 2568, 3080, 4104, 6152,
+                               8200, 10248, 12296])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_many_rows_at_every_count_of_vectors(gpu_lib, d, dtype):
+    # one to four vectors (fp32: eight) a thread, and what three would be in bf16
+    x, gamma, beta, dy = _make(1300, d, dtype, seed=21)
+    _, mean, rstd, kept = _check_forward(gpu_lib, x, gamma, beta, True, checkpoint=True)
+    _check_backward(gpu_lib, dy, x, _np(x), mean, rstd, gamma)
+    _check_backward(gpu_lib, dy, kept, ops_ref.act8(_np(x))[2], mean, rstd, gamma)
