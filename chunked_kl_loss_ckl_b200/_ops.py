@@ -358,8 +358,8 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, stream=Non
     if u.dim() not in (1, 2) or u.shape[0] != T:
         raise ValueError("u must have shape [T] or [T, N]")
     N = 1 if u.dim() == 1 else u.shape[1]
-    if T * N >= _INT32_MAX:
-        raise ValueError("u must have fewer than 2^31 - 1 numbers")
+    if T * N > _INT32_MAX:
+        raise ValueError("u must have fewer than 2^31 numbers")
     if isinstance(top_k, int):  # more than a row has is all of it
         top_k = max(0, min(top_k, _INT32_MAX))
     numbers, rows = [], []

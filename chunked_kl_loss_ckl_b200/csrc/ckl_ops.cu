@@ -483,7 +483,7 @@ int ckl_sample(const uint16_t* logits, int64_t ld, int64_t T, int64_t V, const f
                const float* temperature_rows, const int32_t* top_k_rows, const float* top_p_rows,
                const float* min_p_rows, int32_t* ids, float* logp, int32_t* device_status,
                void* stream) {
-  if (T < 0 || V < 1 || ld < V || N < 1 || T >= kLim / N) return CKL_ERR_INVALID_ARG;
+  if (T < 0 || V < 1 || ld < V || N < 1 || T > kLim / N) return CKL_ERR_INVALID_ARG;
   if (T > 0 && ld > (int64_t(1) << 61) / T) return CKL_ERR_INVALID_ARG;
   if (T > 0 && (!logits || !u || !ids)) return CKL_ERR_INVALID_ARG;
   if (!aligned(logits, 2) || !aligned(u, 4) || !aligned(ids, 4) || !aligned(logp, 4) ||

@@ -776,6 +776,12 @@ __device__ __forceinline__ void sample_find(SampleShared& sm, const SampleSpan& 
   if (lane == 0) *id_out = id;
 }
 
+// Draws of a row, for loops over them in steps: N may be 2^31 - 1, and an int
+// would pass its end with the last step.
+__device__ __forceinline__ uint32_t sample_draws(const SampleParams& p) {
+  return static_cast<uint32_t>(p.N);
+}
+
 __device__ __forceinline__ void sample_put(const SampleParams& p, int64_t row, int n, int id,
                                            float logp) {
   p.ids[row * p.N + n] = id;
@@ -1162,7 +1168,7 @@ sample_kernel(const __grid_constant__ SampleParams p) {
     const bool bad = !r.ok || (flags & SF_BAD);
     if (bad || m == -INFINITY) {  // no answer: bad numbers, or nothing left to draw
       if (rank == 0)
-        for (int n = tid; n < p.N; n += sample_nt()) sample_no_draw(p, row, n);
+        for (uint32_t n = tid; n < sample_draws(p); n += sample_nt()) sample_no_draw(p, row, n);
       if (bad && rank == 0 && tid == 0) sample_bad(p);
       continue;
     }
@@ -1202,7 +1208,7 @@ sample_kernel(const __grid_constant__ SampleParams p) {
     }
     __syncthreads();
     if constexpr (MANY) {
-      for (int n0 = 0; n0 < p.N; n0 += SM_BATCH)
+      for (uint32_t n0 = 0; n0 < sample_draws(p); n0 += SM_BATCH)
         sample_batch<C>(sm, p, row, sp, rank, m, n0);
     } else {
       const uint32_t bin = sm.draw_bin[0];
@@ -1335,7 +1341,7 @@ sample_short_kernel(const __grid_constant__ SampleParams p) {
     }
     const bool bad = !r.ok || flags;
     if (bad || n == 0) {
-      for (int k = tid; k < p.N; k += SM_SHORT_THREADS) sample_no_draw(p, row, k);
+      for (uint32_t k = tid; k < sample_draws(p); k += SM_SHORT_THREADS) sample_no_draw(p, row, k);
       if (bad && tid == 0) sample_bad(p);
       continue;
     }
@@ -1398,7 +1404,7 @@ sample_short_kernel(const __grid_constant__ SampleParams p) {
       L = keep;
     }
     const double mass = cum[L - 1];
-    for (int k = tid; k < p.N; k += SM_SHORT_THREADS) {
+    for (uint32_t k = tid; k < sample_draws(p); k += SM_SHORT_THREADS) {
       const float u = p.u[row * p.N + k];
       if (!sample_u_ok(u)) {
         sample_no_draw(p, row, k);

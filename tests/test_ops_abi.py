@@ -152,3 +152,19 @@ def test_reference_norm_gradients_match_differences():
             e[j] = h
             assert abs((f(x, g + e, b) - f(x, g - e, b)) / (2 * h) - dg[j]) < 1e-7
             assert abs((f(x, g, b + e) - f(x, g, b - e)) / (2 * h) - db[j]) < 1e-7
+
+
+def test_sample_takes_every_count_of_draws_that_the_header_names(ckl):
+    # T N < 2^31; a vocabulary past the largest is refused next, before anything
+    # is launched
+    f = ckl.lib.ckl_sample
+
+    def s(T, draws):
+        return f(F, 1 << 23, T, (1 << 21) + 1, F, draws, 1.0, 0, 1.0, 0.0, N, N, N, N, F, F, N, N)
+
+    top = 2 ** 31 - 1
+    for T, draws in ((1, top), (top, 1), (1, 1 << 30), (2, (1 << 30) - 1), (2, 800_000_000),
+                     (3, 715_827_882), (7, 306_783_378)):
+        assert s(T, draws) == 2, (T, draws)
+    for T, draws in ((1 << 31, 1), (2, 1 << 30), (3, 715_827_883), (top, 2), (46341, 46341)):
+        assert s(T, draws) == 1, (T, draws)
