@@ -45,7 +45,15 @@ namespace ckl {
 
 constexpr int NORM_THREADS = 512;
 constexpr int NORM_WARPS = 16;  // of a block, at most
-constexpr int NORM_MAX_PARTS = 592;  // blocks whose gradient sums the workspace holds
+// Blocks whose gradient sums the workspace holds: one an SM (148 on a B200; a
+// launch takes no more than this, whatever the device has), and where the sums
+// have a kernel of their own (every d above NORM_REGS_D) one for 64 rows, 64 at
+// most.
+constexpr int NORM_MAX_PARTS = 160;
+constexpr int NORM_REGS_D = 16384;
+__host__ __device__ constexpr int64_t norm_cols_parts(int64_t T) {
+  return (T + 63) / 64 < 64 ? (T + 63) / 64 : 64;
+}
 
 struct NormFwd {
   const void* x;

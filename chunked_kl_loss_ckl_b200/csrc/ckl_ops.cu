@@ -146,7 +146,7 @@ constexpr NormShape norm_fwd_shape(int64_t d, int V, bool vec, bool many) {
 constexpr NormShape norm_bwd_shape(int64_t d, int V, bool vec, bool q8, bool many) {
   if (!vec) return norm_shape(d, 1, 8, 16);
   const NormShape s = norm_shape(d, V, 16 / V, 0);
-  if (V == 8 && d <= 16384 && (s.nv == 0 || (!q8 && many && d > 2560)))
+  if (V == 8 && d <= ckl::NORM_REGS_D && (s.nv == 0 || (!q8 && many && d > 2560)))
     return norm_shape(d, V, 4, 0);
   return s;
 }
@@ -180,13 +180,13 @@ constexpr bool norm_shape_ok(const NormShape& s, int64_t n) {
 }
 template <int V>
 constexpr bool norm_fwd_shapes_ok(bool many) {
-  for (int64_t n = 1; n <= 16384 / V + 1; ++n)
+  for (int64_t n = 1; n <= ckl::NORM_REGS_D / V + 1; ++n)
     if (!norm_shape_ok<NormFwdCounts<V>>(norm_fwd_shape(n * V, V, true, many), n)) return false;
   return true;
 }
 template <int V>
 constexpr bool norm_bwd_shapes_ok(bool q8, bool many) {
-  for (int64_t n = 1; n <= 16384 / V + 1; ++n)
+  for (int64_t n = 1; n <= ckl::NORM_REGS_D / V + 1; ++n)
     if (!norm_shape_ok<NormBwdCounts<V>>(norm_bwd_shape(n * V, V, true, q8, many), n)) return false;
   return true;
 }
@@ -198,8 +198,13 @@ static_assert(norm_bwd_shapes_ok<8>(false, false) && norm_bwd_shapes_ok<8>(false
 static_assert(norm_bwd_shapes_ok<4>(false, false) && norm_bwd_shapes_ok<4>(false, true) &&
                   norm_bwd_shapes_ok<4>(true, false) && norm_bwd_shapes_ok<4>(true, true),
               "fp32 backward");
-static_assert(norm_fwd_shape(16385, 8, true, false).nv == 0 &&
-                  norm_fwd_shape(16388, 4, true, false).nv == 0,
+constexpr int64_t kPast = ckl::NORM_REGS_D + 8;
+static_assert(norm_fwd_shape(kPast, 8, true, false).nv == 0 &&
+                  norm_fwd_shape(kPast, 4, true, false).nv == 0 &&
+                  norm_bwd_shape(kPast, 8, true, false, true).nv == 0 &&
+                  norm_bwd_shape(kPast, 8, true, true, true).nv == 0 &&
+                  norm_bwd_shape(kPast, 4, true, false, true).nv == 0 &&
+                  norm_bwd_shape(ckl::NORM_REGS_D + 1, 1, false, false, true).nv == 0,
               "no width behind the checked ones has a shape");
 
 // Of an SM, for the blocks' dynamic shared memory; also the most a block takes
@@ -281,7 +286,7 @@ int norm_bwd_launch(const ckl::NormBwd& p0, bool vec, int sms, cudaStream_t st, 
                        std::max(ring, sums), st);
   };
   if (s.nv != 0) return NormBwdCounts<V>::launch(s.nv, go);
-  parts = static_cast<int>(std::min<int64_t>(cdiv(p.T, 8 * ckl::NORM_COL_WARPS), 64));
+  parts = static_cast<int>(ckl::norm_cols_parts(p.T));
   if (p.want_gamma || p.want_beta) {  // first: dx may take dy's place
     const dim3 cols(static_cast<unsigned>(cdiv(p.d, 32 * (vec ? V : 1))),
                     static_cast<unsigned>(parts));
@@ -415,8 +420,9 @@ int ckl_norm_forward(const void* x, int32_t dtype, const void* gamma, const void
 
 size_t ckl_norm_workspace_bytes(int64_t T, int64_t d) {
   if (!norm_sizes_ok(T, d)) return 0;
-  const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(T, ckl::NORM_MAX_PARTS));
-  return static_cast<size_t>(parts) * 2 * d * 4;
+  const int64_t parts = d > ckl::NORM_REGS_D ? ckl::norm_cols_parts(T)
+                                             : std::min<int64_t>(T, ckl::NORM_MAX_PARTS);
+  return static_cast<size_t>(std::max<int64_t>(1, parts)) * 2 * d * 4;
 }
 
 int ckl_norm_backward(const void* dy, int32_t dtype, const void* x, const int8_t* q,

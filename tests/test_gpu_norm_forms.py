@@ -44,3 +44,20 @@ def test_many_rows_at_every_count_of_vectors(gpu_lib, d, dtype):
     _, mean, rstd, kept = _check_forward(gpu_lib, x, gamma, beta, True, checkpoint=True)
     _check_backward(gpu_lib, dy, x, _np(x), mean, rstd, gamma)
     _check_backward(gpu_lib, dy, kept, ops_ref.act8(_np(x))[2], mean, rstd, gamma)
+
+
+@pytest.mark.parametrize("T,d", [(1, 16392), (65, 20000), (300, 17000), (4200, 16385), (300, 16384),
+                                 (200, 9001), (161, 1001), (1300, 4096)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_workspace_of_just_the_size(gpu_lib, T, d, dtype):
+    x, gamma, beta, dy = _make(T, d, dtype, seed=22)
+    n = gpu_lib.norm_workspace_bytes(T, d)
+    buf = torch.full((n + 8192,), 0xA5, dtype=torch.uint8, device="cuda")
+    _, mean, rstd, kept = gpu_lib.norm_forward(x, gamma, beta, checkpoint=True)
+    for src in (x, kept):
+        ref = gpu_lib.norm_backward(dy, src, mean, rstd, gamma, bias=True)
+        got = gpu_lib.norm_backward(dy, src, mean, rstd, gamma, bias=True, workspace=buf[:n])
+        assert all(torch.equal(a, b) for a, b in zip(ref, got))
+        assert (buf[n:] == 0xA5).all()
+    with pytest.raises(gpu_lib.CklError):
+        gpu_lib.norm_backward(dy, x, mean, rstd, gamma, workspace=buf[:n - 16])

@@ -168,3 +168,16 @@ def test_sample_takes_every_count_of_draws_that_the_header_names(ckl):
         assert s(T, draws) == 2, (T, draws)
     for T, draws in ((1 << 31, 1), (2, 1 << 30), (3, 715_827_883), (top, 2), (46341, 46341)):
         assert s(T, draws) == 1, (T, draws)
+
+
+def test_norm_workspace_is_what_the_sums_take(ckl):
+    # 2 d floats a part: a part an SM (160 at most), and for rows that no thread
+    # holds (d > 16384) a part for 64 rows, 64 at most
+    w = ckl.lib.ckl_norm_workspace_bytes
+    for d in (1, 64, 4096, 16384):
+        for T in (1, 7, 148, 160, 161, 8192, 1 << 30):
+            assert w(T, d) == min(T, 160) * d * 8
+    for d in (16385, 20000, 1 << 20):
+        for T in (1, 64, 65, 1000, 4096, 4097, 1 << 30):
+            assert w(T, d) == min(-(-T // 64), 64) * d * 8
+    assert w(0, 64) == 64 * 8 and w(0, 20000) == 20000 * 8
