@@ -195,12 +195,14 @@ def norm_workspace_bytes(T: int, d: int) -> int:
 
 
 def norm_backward(dy, x, mean, rstd, gamma=None, bias: bool = False, dgamma=None, dbeta=None,
-                  accumulate: bool = False, workspace=None, stream=None, out_dx=None):
+                  accumulate: bool = False, workspace=None, stream=None, out_dx=None,
+                  weight: bool = True):
     """(dx, dgamma, dbeta) of ``norm_forward``, from its mean and rstd.
 
     ``x`` is the forward's input, or what it kept of it, (q, exponents).
-    dgamma (None without gamma) and dbeta (with ``bias``, else None) are fp32
-    [d]; given ones are written, or added to with ``accumulate``.
+    dgamma (None without gamma, or without ``weight``: a gamma that is not
+    trained) and dbeta (with ``bias``, else None) are fp32 [d]; given ones are
+    written, or added to with ``accumulate``.
     """
     _check("dy", dy, _DTYPES)
     T, d = _rows("dy", dy)
@@ -219,11 +221,12 @@ def norm_backward(dy, x, mean, rstd, gamma=None, bias: bool = False, dgamma=None
     for name, t in (("dgamma", dgamma), ("dbeta", dbeta)):
         if t is not None:
             _check(name, t, (torch.float32,), (d,), like=dy)
-    if dgamma is not None and gamma is None:
-        raise ValueError("dgamma without gamma")
+    weight = weight and gamma is not None
+    if dgamma is not None and not weight:
+        raise ValueError("dgamma without gamma, or without weight")
     if dbeta is not None and not bias:
         raise ValueError("dbeta without bias")
-    if accumulate and ((gamma is not None and dgamma is None) or (bias and dbeta is None)):
+    if accumulate and ((weight and dgamma is None) or (bias and dbeta is None)):
         raise ValueError("accumulate needs the gradients that are added to")
     if workspace is not None and (not workspace.is_cuda or workspace.device != dy.device
                                   or workspace.dtype != torch.uint8
@@ -235,7 +238,7 @@ def norm_backward(dy, x, mean, rstd, gamma=None, bias: bool = False, dgamma=None
     def call(st):
         dx = out_dx if out_dx is not None else torch.empty_like(dy)
         dg = dgamma
-        if dg is None and gamma is not None:
+        if dg is None and weight:
             dg = rstd.new_empty(d)
         db = dbeta
         if db is None and bias:
@@ -270,7 +273,8 @@ class _Norm(torch.autograd.Function):
         *x, mean, rstd, gamma = ctx.saved_tensors
         x = tuple(x) if ctx.kept8 else x[0]
         bias = ctx.bias is not None and ctx.needs_input_grad[2]
-        dx, dg, db = norm_backward(dy.contiguous(), x, mean, rstd, gamma, bias=bias)
+        dx, dg, db = norm_backward(dy.contiguous(), x, mean, rstd, gamma, bias=bias,
+                                   weight=ctx.needs_input_grad[1])
         return (dx, None if dg is None else dg.to(gamma.dtype),
                 db.to(ctx.bias) if bias else None, None, None, None)
 
@@ -308,10 +312,14 @@ class _NormKL(torch.autograd.Function):
         gl = g.reshape(1).to(torch.float32).contiguous()
         dH, dW = backward(H, W, idx, logp, mask, lse, grad_loss=gl, chunk=ctx.chunk)
         del H
+        dx = dg = db = None
         bias = beta is not None and ctx.needs_input_grad[2]
-        dx, dg, db = norm_backward(dH, x, mean, rstd, gamma, bias=bias, out_dx=dH)
+        if any(ctx.needs_input_grad[:3]):
+            dx, dg, db = norm_backward(dH, x, mean, rstd, gamma, bias=bias, out_dx=dH,
+                                       weight=ctx.needs_input_grad[1])
         return (dx, None if dg is None else dg.to(gamma.dtype), db.to(beta.dtype) if bias else None,
-                dW.to(W.dtype), None, None, None, None, None, None)
+                dW.to(W.dtype) if ctx.needs_input_grad[3] else None, None, None, None, None, None,
+                None)
 
 
 def norm_kl_loss(x, gamma, beta, W, idx, logp, mask=None, eps: float = 1e-5, center: bool = True,

@@ -61,3 +61,54 @@ def test_a_workspace_of_just_the_size(gpu_lib, T, d, dtype):
         assert (buf[n:] == 0xA5).all()
     with pytest.raises(gpu_lib.CklError):
         gpu_lib.norm_backward(dy, x, mean, rstd, gamma, workspace=buf[:n - 16])
+
+
+def _unused(*a, **kw):
+    raise AssertionError("not asked for")
+
+
+@pytest.mark.parametrize("T,d", [(9, 72), (700, 2880), (1300, 4096), (300, 1001), (70, 20000)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_weight_that_is_not_trained(gpu_lib, monkeypatch, T, d, dtype):
+    # only what is asked for: no sums over the rows, no memory for them
+    x, gamma, beta, dy = _make(T, d, dtype, seed=23)
+    y, mean, rstd, kept = gpu_lib.norm_forward(x, gamma, beta, checkpoint=True)
+    for src in (x, kept):
+        dx, dg, db = gpu_lib.norm_backward(dy, src, mean, rstd, gamma, bias=True)
+        only = gpu_lib.norm_backward(dy, src, mean, rstd, gamma, bias=True, weight=False)
+        assert torch.equal(only[0], dx) and only[1] is None and torch.equal(only[2], db)
+    with pytest.raises(ValueError):
+        gpu_lib.norm_backward(dy, x, mean, rstd, gamma, dgamma=torch.zeros(d, device="cuda"),
+                              weight=False)
+    dx = gpu_lib.norm_backward(dy, x, mean, rstd, gamma)[0]
+    monkeypatch.setattr(gpu_lib._ops, "norm_workspace_bytes", _unused)
+    alone = gpu_lib.norm_backward(dy, x, mean, rstd, gamma, weight=False)
+    assert torch.equal(alone[0], dx) and alone[1:] == (None, None)
+    xs = x.clone().requires_grad_()
+    gpu_lib.layer_norm(xs, gamma, beta).backward(dy)      # gamma and beta are no leaves
+    assert torch.equal(xs.grad, dx) and gamma.grad is None
+
+
+def test_norm_kl_loss_makes_what_needs_a_gradient(gpu_lib, monkeypatch):
+    x, gamma, beta, _ = _make(60, 128, BF, seed=24)
+    W = (torch.randn(500, 128, device="cuda") * 0.1).to(BF)
+    idx = torch.randint(0, 500, (60, 8), device="cuda", dtype=torch.int32)
+    logp = torch.zeros(60, 8, device="cuda")
+    full = [t.clone().requires_grad_() for t in (x, gamma, beta, W)]
+    gpu_lib.norm_kl_loss(*full, idx, logp).backward()
+    for need in ((0,), (1,), (0, 3), (2, 3), (3,)):
+        leaves = [t.clone().requires_grad_(i in need) for i, t in enumerate((x, gamma, beta, W))]
+        with monkeypatch.context() as m:
+            if need == (3,):                              # the head alone: no norm behind it
+                m.setattr(gpu_lib._ops, "norm_backward", _unused)
+            if not {1, 2} & set(need):
+                m.setattr(gpu_lib._ops, "norm_workspace_bytes", _unused)
+            gpu_lib.norm_kl_loss(*leaves, idx, logp).backward()
+        for i, (a, b) in enumerate(zip(leaves, full)):
+            if i not in need:
+                assert a.grad is None
+            else:
+                # the head's fp32 sums (500 terms: 2^-14 of the largest) may be taken
+                # in another order, and a bf16 rounding with them (2^-7 of the value)
+                p, q = a.grad.double(), b.grad.double()
+                assert ((p - q).abs() <= 2.0 ** -7 * q.abs() + 2.0 ** -14 * q.abs().max()).all()
