@@ -6,15 +6,16 @@
 // magnitude a: b = floor(log2 a) + 127 puts a / 2^(b - 133) in [64, 128), one
 // more where that would round to 128.  Both scalings are powers of two, so the
 // only rounding is the one to the integer (nearest, ties to even): an element
-// is off by at most half a step, 2^(b - 134) <= a / 127.  Groups of 32 follow
-// the outlier channels of a residual stream, which a scale per row would not;
-// they cost 1/32 byte an element.  A power of two instead of a / 127 gives up
+// is off by at most half a step, 2^(b - 134) <= max(a / 127, 2^-134).  Groups of
+// 32 follow the outlier channels of a residual stream, which a scale per row would
+// not; they cost 1/32 byte an element.  A power of two instead of a / 127 gives up
 // half a bit on average, and makes the stored values the same whatever order
 // or precision they were computed in; |q| <= 127 is exact in bf16.
-// Subnormal groups use b = 0; b = 255 is never written (its values would pass
-// the largest float), so the largest floats clamp to 127.  An element that is
-// not finite is stored as q = -128 and read back as NaN, and does not count
-// towards its group's scale.
+// Subnormal groups use b = 0 (exact in bf16, whose values are multiples of 2^-133;
+// fp32 magnitudes up to 2^-134 read back as 0); b = 255 is never written (its
+// values would pass the largest float), so the largest floats clamp to 127.  An
+// element that is not finite is stored as q = -128 and read back as NaN, and does
+// not count towards its group's scale.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -41,9 +42,11 @@ __device__ __forceinline__ uint32_t act8_mag(float x) {
 }
 
 // The exponent byte of a group whose largest magnitude has bits `a`: from
-// 1.9921875 x 2^E on, a / 2^(E - 6) >= 127.5 rounds to 128.
+// 1.9921875 x 2^E on, a / 2^(E - 6) >= 127.5 rounds to 128, and the sum carries
+// into the exponent.  Below 2^-126 a has no leading 1: a / 2^-133 is its bits /
+// 2^16, which passes 127.5 half a step later.
 __device__ __forceinline__ uint32_t act8_byte(uint32_t a) {
-  const uint32_t b = (a >> 23) + ((a & 0x7FFFFFu) >= 0x7F0000u ? 1u : 0u);
+  const uint32_t b = (a + (a < 0x800000u ? 0x8000u : 0x10000u)) >> 23;
   return b > 254u ? 254u : b;
 }
 

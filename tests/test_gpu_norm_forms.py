@@ -63,6 +63,54 @@ def test_a_workspace_of_just_the_size(gpu_lib, T, d, dtype):
         gpu_lib.norm_backward(dy, x, mean, rstd, gamma, workspace=buf[:n - 16])
 
 
+@pytest.mark.parametrize("d", [64, 65])
+def test_act8_of_subnormal_groups(gpu_lib, d):
+    g = torch.Generator(device="cuda").manual_seed(d)
+    x = torch.rand(300, d, generator=g, device="cuda", dtype=torch.float64) * 2 - 1
+    x *= torch.exp2(-149 + 29 * torch.rand(300, 1, generator=g, device="cuda", dtype=torch.float64))
+    x = x.to(F32)
+    q, e = gpu_lib.act8_pack(x)
+    rq, re, val = ops_ref.act8(_np(x))
+    assert (q.cpu().numpy() == rq).all() and (e.cpu().numpy() == re).all()
+    for out in (BF, F32):
+        assert (_np(gpu_lib.act8_unpack(q, e, out)) == val).all()
+    # around the largest that b = 0 holds, 127.5 of its steps, and b = 1's: in bf16
+    # every value is one of the steps, and comes back as it is
+    step = torch.tensor([126.0, 127.0, 127.25, 127.5, 127.75, 128.0, 254.0, 254.5, 255.0, 256.0])
+    x = (step.double()[:, None] * 2.0 ** -133).repeat(1, d).cuda()
+    x[:, 1::3] *= -1
+    for dtype in (BF, F32):
+        for center in (None, True, False):               # alone, and kept by a norm's forward
+            xt = x.to(dtype)
+            if center is None:
+                q, e = gpu_lib.act8_pack(xt)
+            else:
+                q, e = gpu_lib.norm_forward(xt, center=center, checkpoint=True)[3]
+            rq, re, val = ops_ref.act8(_np(xt))
+            assert (q.cpu().numpy() == rq).all() and (e.cpu().numpy() == re).all()
+            if dtype == BF:
+                small = (xt[:, 0] < 2.0 ** -126).nonzero()[:, 0]
+                back = gpu_lib.act8_unpack(q, e)
+                assert len(small) and torch.equal(back[small], xt[small])
+
+
+def test_act8_at_every_largest_magnitude(gpu_lib):
+    # every finite bf16 as a group's largest, and fp32's around where a scale ends
+    bits = torch.arange(0x7F80, dtype=torch.int32, device="cuda")
+    tops = (bits << 16).view(F32)
+    mant = torch.tensor([0, 1, 0x400000, 0x7EFFFF, 0x7F0000, 0x7F0001, 0x7F7FFF, 0x7F8000, 0x7F8001,
+                         0x7FFFFF], dtype=torch.int32, device="cuda")
+    fine = ((torch.arange(255, dtype=torch.int32, device="cuda")[:, None] << 23) | mant).view(-1)
+    for top, dtype in ((tops, BF), (fine.view(F32), F32)):
+        part = torch.linspace(-1, 1, 40, device="cuda", dtype=torch.float64)
+        x = (top.double()[:, None] * part).to(dtype)
+        x[:, 5] = top.to(dtype)
+        q, e = gpu_lib.act8_pack(x)
+        rq, re, val = ops_ref.act8(_np(x))
+        assert (q.cpu().numpy() == rq).all() and (e.cpu().numpy() == re).all()
+        assert (_np(gpu_lib.act8_unpack(q, e, dtype)) == val).all()
+
+
 def _unused(*a, **kw):
     raise AssertionError("not asked for")
 
