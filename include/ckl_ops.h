@@ -39,9 +39,10 @@ enum {
  * and the element's value is q 2^(b - 133).  b is the smallest that holds the
  * group's largest magnitude after rounding to the nearest integer (ties to
  * even; at most 254, so the largest floats clamp to 127), so that an element is
- * off by at most the group's largest magnitude / 127.  An element that is not
- * finite is stored as q = -128, reads back as NaN, and does not count towards
- * its group's scale.  Values of q read back exactly in bf16 and fp32.
+ * off by at most the group's largest magnitude / 127, or 2^-134 where that is
+ * more (fp32 groups below 2^-127: the scale goes no lower than 2^-133, bf16's
+ * smallest value).  An element that is not finite is stored as q = -128, reads
+ * back as NaN, and does not count towards its group's scale.  Values of q read back exactly in bf16 and fp32.
  *
  * ckl_act8_pack:   x [T, d] -> q [T, d], exponents [T, groups]
  * ckl_act8_unpack: q, exponents -> x [T, d]

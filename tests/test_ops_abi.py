@@ -181,3 +181,18 @@ def test_norm_workspace_is_what_the_sums_take(ckl):
         for T in (1, 64, 65, 1000, 4096, 4097, 1 << 30):
             assert w(T, d) == min(-(-T // 64), 64) * d * 8
     assert w(0, 64) == 64 * 8 and w(0, 20000) == 20000 * 8
+
+
+def test_reference_act8_bound_of_subnormal_groups():
+    # b = 0 has the smallest step, 2^-133: fp32 groups below 2^-127 are off by up to
+    # half of it, which is more than largest / 127
+    rng = np.random.default_rng(2)
+    x = rng.uniform(-1, 1, (400, 32)) * np.exp2(rng.uniform(-149, -120, (400, 1)))
+    x = x.astype(np.float32).astype(np.float64)
+    x[0] = 1.4 * 2.0 ** -134
+    x[1] = 2.0 ** -134                               # half a step: to even, 0
+    q, e, val = ops_ref.act8(x)
+    top, err = np.abs(x).max(1, keepdims=True), np.abs(val - x)
+    assert (err <= np.maximum(top / 127, 2.0 ** -134)).all()
+    assert (err[0] > 0.4 * x[0]).all() and not val[1].any()
+    assert (e[top[:, 0] < 2.0 ** -127] == 0).all()
