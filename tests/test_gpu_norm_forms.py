@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import ops_ref
+import test_gpu_norm
 from test_gpu_norm import _check_backward, _check_forward, _make, _np
 
 pytestmark = pytest.mark.gpu
@@ -160,3 +161,54 @@ def test_norm_kl_loss_makes_what_needs_a_gradient(gpu_lib, monkeypatch):
                 # in another order, and a bf16 rounding with them (2^-7 of the value)
                 p, q = a.grad.double(), b.grad.double()
                 assert ((p - q).abs() <= 2.0 ** -7 * q.abs() + 2.0 ** -14 * q.abs().max()).all()
+
+
+@pytest.mark.parametrize("T,d", [(400, 72), (400, 2880), (1300, 1280), (1300, 4096), (310, 7176),
+                                 (310, 16384), (400, 1001), (1300, 17), (320, 17000), (300, 8300),
+                                 (300, 9001)])
+@pytest.mark.parametrize("dtype,pdtype", [(BF, BF), (BF, F32), (F32, F32), (F32, BF)])
+def test_many_rows_without_centring_and_with_other_parameters(gpu_lib, T, d, dtype, pdtype):
+    # more rows than keep the parameters in registers: from shared memory, and
+    # where there are none
+    x, gamma, beta, dy = _make(T, d, dtype, seed=25, pdtype=pdtype)
+    val = ops_ref.act8(_np(x))[2]
+    for center, g, b in ((False, gamma, None), (False, None, None), (True, gamma, None),
+                         (True, None, beta), (True, None, None), (False, gamma, beta)):
+        _, mean, rstd, kept = _check_forward(gpu_lib, x, g, b, center, checkpoint=g is not None)
+        _check_backward(gpu_lib, dy, x, _np(x), mean, rstd, g, bias=b is not None)
+        if kept is not None:
+            _check_backward(gpu_lib, dy, kept, val, mean, rstd, g, bias=b is not None)
+
+
+@pytest.mark.parametrize("T,d", [(5000, 8), (3000, 1001), (2000, 96), (1300, 2880), (1300, 2560),
+                                 (1300, 20000), (1300, 9001), (700, 16384), (3000, 64)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_in_place_with_many_rows_a_group(gpu_lib, T, d, dtype):
+    # rows fetched ahead while earlier ones are overwritten
+    x, gamma, beta, dy = _make(T, d, dtype, seed=26)
+    for kept8 in (False, True):
+        y, mean, rstd, kept = gpu_lib.norm_forward(x, gamma, beta, checkpoint=kept8)
+        a = x.clone()
+        got = gpu_lib.norm_forward(a, gamma, beta, checkpoint=kept8, out=a)
+        assert got[0] is a and torch.equal(a, y)
+        assert torch.equal(got[1], mean) and torch.equal(got[2], rstd)
+        if kept8:
+            assert torch.equal(got[3][0], kept[0]) and torch.equal(got[3][1], kept[1])
+        src = kept if kept8 else x
+        ref = gpu_lib.norm_backward(dy, src, mean, rstd, gamma, bias=True)
+        b = dy.clone()
+        got = gpu_lib.norm_backward(b, src, mean, rstd, gamma, bias=True, out_dx=b)
+        assert got[0] is b and all(torch.equal(p, q) for p, q in zip(got, ref))
+
+
+@pytest.mark.parametrize("d", [32767, 65536, 100003])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_very_long_rows(gpu_lib, monkeypatch, d, dtype):
+    # a thread adds d / 512 values of a row in a chain, beside the 40 adds over
+    # the block and the further operations of test_gpu_norm.py's bound
+    monkeypatch.setattr(test_gpu_norm, "C", (-(-d // 512) + 100) * ops_ref.U32)
+    x, gamma, beta, dy = _make(70, d, dtype, seed=27)
+    for center in (True, False):
+        _, mean, rstd, kept = _check_forward(gpu_lib, x, gamma, beta, center, checkpoint=True)
+        _check_backward(gpu_lib, dy, x, _np(x), mean, rstd, gamma)
+        _check_backward(gpu_lib, dy, kept, ops_ref.act8(_np(x))[2], mean, rstd, gamma)
