@@ -212,3 +212,80 @@ def test_very_long_rows(gpu_lib, monkeypatch, d, dtype):
         _, mean, rstd, kept = _check_forward(gpu_lib, x, gamma, beta, center, checkpoint=True)
         _check_backward(gpu_lib, dy, x, _np(x), mean, rstd, gamma)
         _check_backward(gpu_lib, dy, kept, ops_ref.act8(_np(x))[2], mean, rstd, gamma)
+
+
+@pytest.mark.parametrize("center", [True, False])
+def test_norm_kl_loss_captured(gpu_lib, center):
+    # each replay gives the gradients of what the buffers then hold
+    x, gamma, beta, _ = _make(200, 128, BF, seed=28)
+    W = (torch.randn(1000, 128, device="cuda") * 0.1).to(BF)
+    idx = torch.randint(0, 1000, (200, 16), device="cuda", dtype=torch.int32)
+    logp = torch.log_softmax(torch.randn(200, 16, device="cuda"), 1)
+
+    def step(*t):
+        leaves = [v.requires_grad_() for v in t]
+        xs, gs, Ws = leaves[0], leaves[1], leaves[-1]
+        loss = gpu_lib.norm_kl_loss(xs, gs, leaves[2] if center else None, Ws, idx, logp,
+                                    center=center, chunk=64)
+        return [loss.detach()] + list(torch.autograd.grad(loss, leaves))
+
+    data = (x, gamma, beta, W) if center else (x, gamma, W)
+    ref = step(*[t.clone() for t in data])
+    held = [torch.zeros_like(t) for t in data]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step(*[t.detach() for t in held])
+    for _ in range(2):
+        for h, t in zip(held, data):
+            h.copy_(t)
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, ref):
+            a, b = a.double(), b.double()
+            assert ((a - b).abs() <= 2.0 ** -7 * b.abs() + 2.0 ** -14 * b.abs().max()).all()
+
+
+def test_one_row_without_leading_dimensions_and_three(gpu_lib):
+    x, gamma, beta, dy = _make(6, 48, F32, seed=29)
+    for shape in ((2, 1, 3, 48), (6, 48)):
+        xs, gs, bs = (t.clone().requires_grad_() for t in (x.view(shape), gamma, beta))
+        y = gpu_lib.layer_norm(xs, gs, bs)
+        y.backward(dy.view(shape))
+        if shape == (2, 1, 3, 48):
+            first = (y, xs.grad, gs.grad, bs.grad)
+    assert all(torch.equal(a.reshape(b.shape), b)
+               for a, b in zip(first, (y, xs.grad, gs.grad, bs.grad)))
+    one = x[0].clone().requires_grad_()
+    y1 = gpu_lib.rms_norm(one, gamma, checkpoint=True)
+    y1.backward(dy[0])
+    assert one.grad.shape == (48,)
+    y2, _, r, kept = gpu_lib.norm_forward(x[:1], gamma, None, 1e-6, False, True)
+    assert torch.equal(y1, y2[0])
+    dx = gpu_lib.norm_backward(dy[:1], kept, None, r, gamma)[0]
+    assert torch.equal(one.grad, dx[0])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d", [64, 4096, 16384, 20000])
+def test_arrays_at_any_element(gpu_lib, d, dtype):
+    # whole vectors of elements at addresses that no vector has
+    x, gamma, beta, dy = _make(7, d, dtype, seed=30)
+
+    def at(t, k):
+        b = torch.empty(t.numel() + k, dtype=t.dtype, device="cuda")[k:].view(t.shape)
+        return b.copy_(t)
+
+    q, e = gpu_lib.act8_pack(x)
+    q1, e1 = gpu_lib.act8_pack(at(x, 1))
+    assert torch.equal(q, q1) and torch.equal(e, e1)
+    y, mean, rstd, kept = gpu_lib.norm_forward(x, gamma, beta, checkpoint=True)
+    assert torch.equal(kept[0], q) and torch.equal(kept[1], e)
+    for k in (1, 3, 4):
+        qs, es = at(q, k), at(e, k)
+        for out in (BF, F32):
+            assert torch.equal(gpu_lib.act8_unpack(qs, es, out), gpu_lib.act8_unpack(q, e, out))
+        _check_backward(gpu_lib, dy, (qs, es), ops_ref.act8(_np(x))[2], mean, rstd, gamma)
+        _check_backward(gpu_lib, dy, at(x, k), _np(x), mean, rstd, gamma)
+        _check_forward(gpu_lib, x, at(gamma, k), beta, True, checkpoint=True)
+        _check_forward(gpu_lib, x, gamma, beta, True, out=at(torch.zeros_like(x), k))
