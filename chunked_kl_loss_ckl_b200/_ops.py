@@ -324,9 +324,10 @@ class _NormKL(torch.autograd.Function):
 
 def norm_kl_loss(x, gamma, beta, W, idx, logp, mask=None, eps: float = 1e-5, center: bool = True,
                  chunk: int = 1024):
-    """``chunked_kl_loss`` of H = norm(x), differentiable in x, gamma, beta and
-    W.  Between the passes it keeps x alone: the backward makes H again, as it
-    makes the logits again, so T x d hidden states are not held twice."""
+    """``chunked_kl_loss`` of H = norm(x), x and W in bf16, differentiable in x,
+    gamma, beta and W.  Between the passes it keeps x alone: the backward makes H
+    again, as it makes the logits again, so T x d hidden states are not held
+    twice.  (``layer_norm`` says what a capture of both passes needs.)"""
     _check("x", x, (torch.bfloat16,))
     for name, t in (("W", W), ("topk_idx", idx), ("topk_logp", logp), ("mask", mask)):
         if t is not None and t.get_device() != x.get_device():
@@ -348,7 +349,8 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, stream=Non
     logit or a parameter out of range, a draw whose number is, and a row
     without a finite logit give id -1 and log-prob NaN; the first two also set
     SAMPLE_BAD_INPUT in ``status`` (an int32 [1] tensor that the caller
-    cleared), when given.
+    cleared), when given.  Rows with logits of 256 and more, or other than 0
+    below 2^-40 in magnitude, are far slower (``include/ckl_ops.h``).
 
     N draws a row are a teacher cache: ``forward(H, W, ids, zeros, ...)``.
     """

@@ -31,11 +31,16 @@
 //
 // On a B200 (share of the copy bandwidth, 6.54 TB/s): forward 16384 x 4096 bf16
 // 48 us (0.86), 4096 x 8192 fp32 43 to 45 us (0.91 to 0.96); backward 68 us
-// (0.91); forward with the 8-bit copy 63 us (0.82); backward from it 74 us (0.70:
-// the bytes' conversion, the issue slots are 61 % taken); backward 4096 x 16384
-// 83 us (0.75), from 8 bits 127 us (0.41).  A row's fixed cost is what short rows
-// pay: backward 131072 x 256 50 us (0.62).  Element-wise rows are bound by
-// instructions: 16384 x 1001 bf16 43 us forward (0.23), 45 us backward (0.33).
+// (0.91); forward with the 8-bit copy 63 us (0.82); backward from it 74 us (0.70);
+// backward 4096 x 16384 83 us (0.75), from 8 bits 127 us (0.41; 72 bytes of spills
+// a thread).  The backward from 8 bits is bound by latency: no unit is above 61 %
+// (issue slots), with a quarter of the SM's warps.  A row's fixed cost is what
+// short rows pay: backward 131072 x 256 50 us (0.62).  Element-wise rows are bound
+// by the instructions that two bytes at a time take: 16384 x 1001 bf16 43 us
+// forward (0.23), 45 us backward (0.33); their backward from 8 bits spills (436
+// bytes a thread above 4096 columns).  Long rows, launch included: 4096 x 20000
+// bf16 100 us forward (0.50), 188 us backward (0.40); 1024 x 100003 801 and 805 us
+// (0.08 and 0.12: element-wise).
 #pragma once
 
 #include "ckl_act8.cuh"

@@ -19,7 +19,9 @@
 //
 // The counters cover |z| in [2^-40, 256) and zero: 2 x 6144 + 1 bins in order.
 // A row with other finite values takes them in eight windows of 8192 keys
-// instead (sample_row_any), unless all of them are so far below the largest
+// instead (sample_row_any: one block, eight passes over the row and one more for
+// every chunk looked into; 128256 logits 1.2 ms with one draw, 9 ms with 64, 296
+// such rows 1.3 and 11 ms), unless all of them are so far below the largest
 // logit (2^-64 of its weight) that their mass, under 2^-40 of the row's, is
 // never reached by a u of 24 bits.
 //
