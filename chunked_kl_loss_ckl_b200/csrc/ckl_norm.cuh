@@ -37,7 +37,7 @@
 // (issue slots), with a quarter of the SM's warps.  A row's fixed cost is what
 // short rows pay: backward 131072 x 256 50 us (0.62).  Element-wise rows are bound
 // by the instructions that two bytes at a time take: 16384 x 1001 bf16 43 us
-// forward (0.23), 45 us backward (0.33); their backward from 8 bits spills (436
+// forward (0.23), 42 us backward (0.36); their backward from 8 bits spills (472
 // bytes a thread above 4096 columns).  Long rows, launch included: 4096 x 20000
 // bf16 100 us forward (0.50), 188 us backward (0.40); 1024 x 100003 801 and 805 us
 // (0.08 and 0.12: element-wise).
@@ -565,9 +565,12 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_bwd_kernel(const NormBwd p)
   const float inv_d = 1.f / static_cast<float>(p.d);
   const int step = p.tpr * VEC;  // columns from a thread's vector to its next
   const int col0 = t * VEC;
-  // only a thread's last vector may be past the row's end: dy and x are zeros
-  // there, which adds nothing to a sum
+  // only a thread's last vector may be past the row's end: dy is zeros there, which
+  // adds nothing to a sum as long as xh is finite where the row's is.  So x is one
+  // of the row's own vectors then (`elsewhere`: the thread's first, or the row's;
+  // VEC = 1: the row's last) and not zeros, whose mean r may pass the largest float.
   auto on = [&](int i) { return (VEC > 1 && i < NV - 1) || col0 + i * step < p.d; };
+  const int elsewhere = NV > 1 ? 0 : -col0;
   Lane<VEC> dg[NV], db[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
@@ -588,14 +591,13 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_bwd_kernel(const NormBwd p)
         const TX* dy = static_cast<const TX*>(p.dy) + at_in;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          const int o = on(i) ? i * step : 0;
+          const int o = on(i) ? i * step : elsewhere;
           cp_async16(smem_u32(mine) + off + i * piece, dy + o, on(i) ? 16u : 0u);
           if constexpr (Q8)
-            cp_async_bytes<VEC>(smem_u32(mine8) + off + i * blockDim.x * VEC, p.q + at_in + o,
-                                on(i) ? VEC : 0u);
+            cp_async_bytes<VEC>(smem_u32(mine8) + off + i * blockDim.x * VEC, p.q + at_in + o, VEC);
           else
             cp_async16(smem_u32(mine) + off + (NV + i) * piece,
-                       static_cast<const TX*>(p.x) + at_in + o, on(i) ? 16u : 0u);
+                       static_cast<const TX*>(p.x) + at_in + o, 16u);
         }
         row_in += stride;
         at_in += stride * p.d;
@@ -616,17 +618,17 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_bwd_kernel(const NormBwd p)
     if constexpr (Q8 && VEC > 1) {
       const uint8_t* e = p.e + r * p.groups + col0 / 32;
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (on(i)) e_next[i] = e[i * (step / 32)];  // step is a multiple of 128
+      for (int i = 0; i < NV; ++i)  // step is a multiple of 128
+        e_next[i] = e[on(i) ? i * (step / 32) : NV > 1 ? 0 : -(col0 / 32)];
     }
     if constexpr (VEC == 1) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = on(i) ? col0 + i * step : 0;
+        const int c = on(i) ? col0 + i * step : p.d - 1;
         Lane<1> x;
         norm_load_x<TX, 1, Q8>(p, r, c, x);
         const float dy = to_f32(static_cast<const TX*>(p.dy)[r * p.d + c]);
-        x_next[i] = on(i) ? x.e[0] : 0.f;
+        x_next[i] = x.e[0];
         dy_next[i] = on(i) ? dy : 0.f;
       }
     }

@@ -289,3 +289,22 @@ def test_arrays_at_any_element(gpu_lib, d, dtype):
         _check_backward(gpu_lib, dy, at(x, k), _np(x), mean, rstd, gamma)
         _check_forward(gpu_lib, x, at(gamma, k), beta, True, checkpoint=True)
         _check_forward(gpu_lib, x, gamma, beta, True, out=at(torch.zeros_like(x), k))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d", [40, 17, 33, 320, 1280])
+def test_backward_of_a_large_constant_row(gpu_lib, d, dtype):
+    # mean r passes the largest float; the row's own x - mean is 0, so xh is 0 and
+    # dx = r (a - mean(a)); what stands behind the row must not count
+    for T in (3, 700):
+        x, gamma, beta, dy = _make(T, d, dtype, seed=31)
+        x[1] = 2.0 ** 110
+        _, mean, rstd, kept = gpu_lib.norm_forward(x, gamma, beta, eps=1e-12, checkpoint=True)
+        assert mean[1] == 2.0 ** 110 and rstd[1] > 9e5
+        r, a = _np(rstd)[1], _np(dy)[1] * _np(gamma)
+        ref = r * (a - a.mean())
+        for src in (x, kept):
+            dx, dg, db = gpu_lib.norm_backward(dy, src, mean, rstd, gamma, bias=True)
+            tol = 1.01 * ops_ref.HALF[dtype] * abs(ref) + 100 * ops_ref.U32 * r * (abs(a) + abs(a).mean())
+            assert (abs(_np(dx)[1] - ref) <= tol).all()
+            assert torch.isfinite(dx).all() and torch.isfinite(dg).all()
