@@ -33,7 +33,7 @@
 // 48 us (0.86), 4096 x 8192 fp32 43 to 45 us (0.91 to 0.96); backward 68 us
 // (0.91); forward with the 8-bit copy 63 us (0.82); backward from it 74 us (0.70);
 // backward 4096 x 16384 83 us (0.75), from 8 bits 127 us (0.41; 72 bytes of spills
-// a thread).  The backward from 8 bits is bound by latency: no unit is above 61 %
+// a thread).  The backward from 8 bits is bound by latency: no unit is above 62 %
 // (issue slots), with a quarter of the SM's warps.  A row's fixed cost is what
 // short rows pay: backward 131072 x 256 50 us (0.62).  Element-wise rows are bound
 // by the instructions that two bytes at a time take: 16384 x 1001 bf16 43 us
